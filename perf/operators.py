@@ -296,11 +296,11 @@ def run(state):
         y = c2d.selective_scan_step(s["x"], s["dt"], s["A"], s["B"], s["C"], state=s["state"], skip=s["skip"], gate=s["gate"],
                                     dt_bias=s["dt_bias"], softplus=True, slots=s["slots"])
         return [y, s["state"]]
-    packed = {"seq_offsets": s["offsets"], "max_len": s["max_len"]} if s["case"]["packed"] else {}
+    packed = {"seq_offsets": s["offsets"]} if s["case"]["packed"] else {}
     if op == "conv":
         return [c2d.causal_conv1d(s["x"], s["w"], s["bias"], state=s["state"], slots=s["slots"], act="silu", **packed), s["state"]]
     y = c2d.selective_scan(s["x"], s["dt"], s["A"], s["B"], s["C"], state=s["state"], skip=s["skip"], gate=s["gate"],
-                           dt_bias=s["dt_bias"], softplus=True, slots=s["slots"], **packed)
+                           dt_bias=s["dt_bias"], softplus=True, slots=s["slots"], longest=s["max_len"], **packed)
     return [y, s["state"]]
 
 
