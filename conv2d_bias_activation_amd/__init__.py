@@ -31,7 +31,8 @@ __all__ = ["conv2d_fused", "conv2d_fused_maxpool3x3s2", "maxpool3x3s2", "avgpool
            "last_error", "library_path", "Conv2dError", "ACT_NONE", "ACT_RELU", "ACT_SILU",
            "workspace_size", "stack_workspace_size", "set_workspace", "DEFAULT_WORKSPACE_BYTES",
            "ACT_PRELU", "RES_BEFORE_ACT", "LAYOUT_NHWC", "LAYOUT_NCHW", "DTYPE_F32",
-           "DTYPE_BF16", "DTYPE_F16"]
+           "DTYPE_BF16", "DTYPE_F16", "causal_conv1d", "causal_conv1d_step", "selective_scan",
+           "selective_scan_step", "w4_pack", "matvec_w4", "W4Weights"]
 
 # Codes of include/conv2d_fused.h
 LAYOUT_NHWC, LAYOUT_NCHW = 0, 1
@@ -101,6 +102,17 @@ SIGNATURES = {
     "conv2d_abi_version": (_i, []),
 }
 
+# The same for include/sequence_ops.h, whose calls take the address of a filled struct.
+SEQUENCE_SIGNATURES = {
+    "causal_conv1d": (_i, [_cp, _vp]),
+    "causal_conv1d_step": (_i, [_cp, _vp]),
+    "selective_scan": (_i, [_cp, _vp]),
+    "selective_scan_step": (_i, [_cp, _vp]),
+    "matvec_w4_packed_bytes": (_i, [_i] * 4 + [ctypes.POINTER(ctypes.c_size_t)]),
+    "matvec_w4_pack": (_i, [_vp] * 4 + [_i] * 4 + [_vp]),
+    "matvec_w4": (_i, [_cp, _vp]),
+}
+
 _lib = None
 
 
@@ -123,7 +135,7 @@ def _load():
             f"{_LIB_PATH} is not built; run `python -c 'import __graft_entry__ as g; g.build()'` "
             "(hipcc --offload-arch=gfx950)")
     lib = ctypes.CDLL(_LIB_PATH)
-    for name, (res, args) in SIGNATURES.items():
+    for name, (res, args) in (*SIGNATURES.items(), *SEQUENCE_SIGNATURES.items()):
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
@@ -769,3 +781,7 @@ def weights_to_ohwi(w, stream=None):
     w2 = torch.empty((Cout, kh, kw, Cin), dtype=w.dtype, device=w.device)
     _check(lib.conv2d_weights_to_ohwi(_ptr(w), _ptr(w2), Cout, Cin, kh, kw, dt, _stream_handle(stream)))
     return w2
+
+
+from .sequence import (W4Weights, causal_conv1d, causal_conv1d_step, matvec_w4, selective_scan,  # noqa: E402
+                       selective_scan_step, w4_pack)

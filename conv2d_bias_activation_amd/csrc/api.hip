@@ -14,12 +14,13 @@
 
 #include "common.hpp"
 #include "kernels.hpp"
+#include "runtime.hpp"
 
 namespace {
-
-using namespace c2d;
-
 thread_local std::string g_err;
+}  // namespace
+
+namespace c2d {
 
 int set_error(int code, const char *fmt, ...) {
     char buf[512];
@@ -48,6 +49,16 @@ int dtype_bytes(int dtype) {
     }
 }
 
+int hip_fail(hipError_t e, const char *what) {
+    return set_error(CONV2D_EHIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+}  // namespace c2d
+
+namespace {
+
+using namespace c2d;
+
 const char *dtype_name(int dtype) {
     switch (dtype) {
     case CONV2D_DTYPE_F32:
@@ -67,14 +78,6 @@ int out_dim(int in, int k, int s, int p) {
     if (span < 0) return -1;
     long long o = span / s + 1;
     return o > 0x7fffffff ? -1 : (int)o;
-}
-
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
-bool overlap(const void *a, long long abytes, const void *b, long long bbytes) {
-    if (!a || !b) return false;
-    uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-    return a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
 }
 
 constexpr long long kMaxElems = 0x7fffffffll;
@@ -176,11 +179,8 @@ struct Plan {
 // of a conv + max pool that runs as two kernels, and a transposed conv's packed
 // weights. Without one (or when it is too small) every call takes a variant that
 // needs no scratch, or returns CONV2D_EUNSUPPORTED where none exists.
-struct Workspace {
-    char *p;
-    size_t bytes;
-};
 constexpr int kMaxDevices = 64;
+std::atomic<int> g_cus[kMaxDevices];  // device_cus' answers
 thread_local Workspace g_ws[kMaxDevices];
 // a planning-only stand-in for "as much workspace as the preferred variants want"
 constexpr size_t kUnlimitedWs = (size_t)1 << 50;
@@ -193,13 +193,14 @@ int ws_slot() {
     return dev;
 }
 
+}  // namespace
+
+namespace c2d {
+
 Workspace current_ws() {
     const int dev = ws_slot();
     return dev >= 0 && dev < kMaxDevices ? g_ws[dev] : Workspace{nullptr, 0};
 }
-
-// Compute units of the current device (queried once per device).
-std::atomic<int> g_cus[kMaxDevices];
 
 int device_cus(int *out) {
     int dev = 0;
@@ -215,6 +216,10 @@ int device_cus(int *out) {
     *out = n;
     return CONV2D_OK;
 }
+
+}  // namespace c2d
+
+namespace {
 
 const char *tile_name(int t) {
     switch (t) {
@@ -650,10 +655,6 @@ int describe(const Plan &p, int layout, int dtype, char *buf, int cap) {
         buf[cap - 1] = 0;
     }
     return n;
-}
-
-int hip_fail(hipError_t e, const char *what) {
-    return set_error(CONV2D_EHIP, "%s: %s", what, hipGetErrorString(e));
 }
 
 int check_pool(const void *x, const void *y, int N, int H, int W, int C, int layout, int dtype,

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "common.hpp"
+#include "../../include/sequence_ops.h"
 
 namespace c2d {
 
@@ -226,5 +227,14 @@ hipError_t launch_deconv_direct(const DeconvArgs &a, int dtype, bool out_f32, bo
 // all pointers 16-byte aligned.
 hipError_t launch_concat(const void *a, const void *b, void *y, int N, int H, int W, int Ca, int Cb, bool up,
                          bool nchw, int dtype, bool vec, hipStream_t st);
+
+// Sequence operators (include/sequence_ops.h), on validated arguments. vec: channels and every
+// stride a multiple of the 16-byte vector and all pointers 16-byte aligned.
+hipError_t launch_causal_conv(const causal_conv1d_args &a, bool vec, bool step, hipStream_t st);
+hipError_t launch_scan(const selective_scan_args &a, bool step, hipStream_t st);
+size_t w4_packed_bytes(int out_features, int in_features, int group, bool zeros);
+hipError_t launch_w4_pack(const void *codes, const void *scales, const void *zeros, void *packed, int out_features,
+                          int in_features, int group, int dtype, hipStream_t st);
+hipError_t launch_matvec_w4(const matvec_w4_args &a, hipStream_t st);
 
 }  // namespace c2d
