@@ -107,6 +107,7 @@ SEQUENCE_SIGNATURES = {
     "causal_conv1d": (_i, [_cp, _vp]),
     "causal_conv1d_step": (_i, [_cp, _vp]),
     "selective_scan": (_i, [_cp, _vp]),
+    "selective_scan_workspace_size": (_i, [_cp, ctypes.POINTER(ctypes.c_size_t)]),
     "selective_scan_step": (_i, [_cp, _vp]),
     "matvec_w4_packed_bytes": (_i, [_i] * 4 + [ctypes.POINTER(ctypes.c_size_t)]),
     "matvec_w4_pack": (_i, [_vp] * 4 + [_i] * 4 + [_vp]),

@@ -231,7 +231,9 @@ hipError_t launch_concat(const void *a, const void *b, void *y, int N, int H, in
 // Sequence operators (include/sequence_ops.h), on validated arguments. vec: channels and every
 // stride a multiple of the 16-byte vector and all pointers 16-byte aligned.
 hipError_t launch_causal_conv(const causal_conv1d_args &a, bool vec, bool step, hipStream_t st);
-hipError_t launch_scan(const selective_scan_args &a, bool step, hipStream_t st);
+size_t scan_workspace(const selective_scan_args &a);  // bytes that its preferred split wants
+hipError_t launch_scan(const selective_scan_args &a, void *ws, size_t ws_bytes, hipStream_t st);
+hipError_t launch_scan_token(const selective_scan_args &a, hipStream_t st);
 size_t w4_packed_bytes(int out_features, int in_features, int group, bool zeros);
 hipError_t launch_w4_pack(const void *codes, const void *scales, const void *zeros, void *packed, int out_features,
                           int in_features, int group, int dtype, hipStream_t st);

@@ -145,8 +145,8 @@ int run_conv(const causal_conv1d_args *args, bool step, void *stream) {
     return e == hipSuccess ? set_ok() : hip_fail(e, op);
 }
 
-int run_scan(const selective_scan_args *args, bool step, void *stream) {
-    const char *op = step ? "selective_scan_step" : "selective_scan";
+// Validates a scan's arguments.
+int check_scan(const selective_scan_args *args, const char *op, bool step) {
     if (!args) return set_error(CONV2D_EINVAL, "%s: args must not be null", op);
     const selective_scan_args &a = *args;
     Shape s{op, a.tokens, a.nseq, a.dtype, false, step};
@@ -161,7 +161,7 @@ int run_scan(const selective_scan_args *args, bool step, void *stream) {
     if (!a.a) return set_error(CONV2D_EINVAL, "%s: a must not be null", op);
     if (!aligned_floats({a.a, a.skip, a.dt_bias}))
         return set_error(CONV2D_EINVAL, "%s: a, skip or dt_bias is not aligned to its type", op);
-    if (s.nseq == 0) return set_ok();
+    if (s.nseq == 0) return CONV2D_OK;
     const long long gn = (long long)a.groups * a.states;
     const Rows rows[] = {{"u", a.u, a.u_batch, a.u_token, a.channels}, {"dt", a.dt, a.dt_batch, a.dt_token, a.channels},
                          {"b", a.b, a.b_batch, a.b_token, gn},         {"c", a.c, a.c_batch, a.c_token, gn},
@@ -183,8 +183,20 @@ int run_scan(const selective_scan_args *args, bool step, void *stream) {
     rc = check_no_overlap(op, ey, {in[0], in[1], in[2], in[3], in[5], es, ea, ek, eb, eo, el});
     if (!rc) rc = check_no_overlap(op, es, {in[0], in[1], in[2], in[3], in[5], ea, ek, eb, eo, el});
     if (rc) return rc;
-    if (((long long)a.channels * a.states / 256 + a.groups + 1) * s.nseq >= kMaxBlocks) return too_many_blocks(op);
-    const hipError_t e = launch_scan(a, step, static_cast<hipStream_t>(stream));
+    // an upper bound of the workgroups of either kernel (a split prompt adds at most 4096 chunks)
+    if (((long long)a.channels * (step ? a.states : 4) / 256 + a.groups + 1) * (2ll * s.nseq + 4096) >= kMaxBlocks)
+        return too_many_blocks(op);
+    return CONV2D_OK;
+}
+
+int run_scan(const selective_scan_args *args, bool step, void *stream) {
+    const char *op = step ? "selective_scan_step" : "selective_scan";
+    const int rc = check_scan(args, op, step);
+    if (rc) return rc;
+    if (args->nseq == 0) return set_ok();
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const Workspace ws = step ? Workspace{} : current_ws();
+    const hipError_t e = step ? launch_scan_token(*args, st) : launch_scan(*args, ws.p, ws.bytes, st);
     return e == hipSuccess ? set_ok() : hip_fail(e, op);
 }
 
@@ -207,6 +219,16 @@ extern "C" {
 int causal_conv1d(const causal_conv1d_args *args, void *stream) { return run_conv(args, false, stream); }
 int causal_conv1d_step(const causal_conv1d_args *args, void *stream) { return run_conv(args, true, stream); }
 int selective_scan(const selective_scan_args *args, void *stream) { return run_scan(args, false, stream); }
+
+int selective_scan_workspace_size(const selective_scan_args *args, size_t *bytes) {
+    const char *op = "selective_scan_workspace_size";
+    if (!bytes) return set_error(CONV2D_EINVAL, "%s: bytes must not be null", op);
+    const int rc = check_scan(args, op, false);
+    if (rc) return rc;
+    *bytes = args->nseq ? scan_workspace(*args) : 0;
+    return set_ok();
+}
+
 int selective_scan_step(const selective_scan_args *args, void *stream) { return run_scan(args, true, stream); }
 
 int matvec_w4_packed_bytes(int out_features, int in_features, int group, int has_zeros, size_t *bytes) {

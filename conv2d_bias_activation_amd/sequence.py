@@ -18,7 +18,7 @@ import struct
 
 import torch
 
-from . import _ACTS, _DTYPES, RES_BEFORE_ACT, _check, _load
+from . import _ACTS, _DTYPES, RES_BEFORE_ACT, _check, _load, _use_workspace
 
 __all__ = ["causal_conv1d", "causal_conv1d_step", "selective_scan", "selective_scan_step", "w4_pack", "matvec_w4",
            "W4Weights"]
@@ -51,6 +51,14 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):  # so that the allocator reuses the memory after this stream's work
         return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _scratch(device, stream, workspace, need):
+    """Registers the workspace of a call; the default one is allocated on the call's stream, so
+    that one that has to grow is freed behind the work that still uses it."""
+    st = _stream_of(device, stream)
+    with torch.cuda.stream(st):
+        _use_workspace(device, st, workspace, need)
 
 
 def _fail(name, what):
@@ -173,7 +181,7 @@ def causal_conv1d_step(x, w, bias=None, alpha=None, *, state, act="none", slots=
 
 
 def _scan(name, u, dt, A, B, C, skip, gate, dt_bias, softplus, state, slots, fresh, seq_offsets, longest, out, stream,
-          step):
+          workspace, step):
     code = _storage(u, "u")
     dev, dtype, shape = u.device, u.dtype, u.shape
     nseq, tokens, u_batch, u_token = _geometry(u, seq_offsets, step, "u")
@@ -202,15 +210,24 @@ def _scan(name, u, dt, A, B, C, skip, gate, dt_bias, softplus, state, slots, fre
     if out is None:
         out = _empty(shape, dtype, dev, stream)
     yp = _rows("out", out, shape, dtype, dev)
-    _call(name, _SCAN.pack(up, dp, Ap, bp, cp, kp, gp, tp, sp, yp, op, lp, u_batch, u_token, *_strides(dt, u),
-                           *_strides(B, u), *_strides(C, u), *((0, 0) if gate is None else _strides(gate, u)),
-                           *_strides(out, u), tokens, longest or 0, nseq, rows, channels, groups, states,
-                           1 if softplus else 0, code, 1 if fresh else 0), dev, stream)
+    args = _SCAN.pack(up, dp, Ap, bp, cp, kp, gp, tp, sp, yp, op, lp, u_batch, u_token, *_strides(dt, u),
+                      *_strides(B, u), *_strides(C, u), *((0, 0) if gate is None else _strides(gate, u)),
+                      *_strides(out, u), tokens, longest or 0, nseq, rows, channels, groups, states,
+                      1 if softplus else 0, code, 1 if fresh else 0)
+    if not step:
+        need = 0
+        if workspace is None:
+            size = ctypes.c_size_t(0)
+            _check(_load().selective_scan_workspace_size(args, ctypes.byref(size)))
+            need = size.value
+        if need or workspace is not None:
+            _scratch(dev, stream, workspace, need)
+    _call(name, args, dev, stream)
     return out
 
 
 def selective_scan(u, dt, A, B, C, *, skip=None, gate=None, dt_bias=None, softplus=False, state=None, slots=None,
-                   fresh=False, seq_offsets=None, longest=None, out=None, stream=None):
+                   fresh=False, seq_offsets=None, longest=None, out=None, stream=None, workspace=None):
     """Selective state space scan along each sequence. With d = dt + dt_bias (through
     log(1 + exp(d)) with ``softplus``), h the [channels, states] state and g a channel's group:
 
@@ -222,17 +239,19 @@ def selective_scan(u, dt, A, B, C, *, skip=None, gate=None, dt_bias=None, softpl
     all of one dtype (float32, bfloat16 or float16), any strides before the last. A [channels,
     states], skip and dt_bias [channels]: float32. ``state`` float32 [rows, channels, states] is
     read and updated in place; ``slots`` and ``fresh`` as for causal_conv1d. ``longest``: tokens
-    of the longest packed sequence where known; it only steers how the work is split. Returns y,
-    shaped as u."""
+    of the longest packed sequence where known; it only steers how the work is split. A split
+    call keeps its chunks' states in the workspace (``workspace`` as everywhere in the binding;
+    False: never split; inside a graph capture pass a tensor that lives as long as the graph).
+    Returns y, shaped as u."""
     return _scan("selective_scan", u, dt, A, B, C, skip, gate, dt_bias, softplus, state, slots, fresh, seq_offsets,
-                 longest, out, stream, False)
+                 longest, out, stream, workspace, False)
 
 
 def selective_scan_step(u, dt, A, B, C, *, state, skip=None, gate=None, dt_bias=None, softplus=False, slots=None,
                         out=None, stream=None):
     """selective_scan for one token of each sequence: u [sequences, channels], B [sequences, groups, states]."""
     return _scan("selective_scan_step", u, dt, A, B, C, skip, gate, dt_bias, softplus, state, slots, False, None, None,
-                 out, stream, True)
+                 out, stream, False, True)
 
 
 class W4Weights:

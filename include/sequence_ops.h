@@ -96,6 +96,12 @@ typedef struct selective_scan_args {
 
 int selective_scan(const selective_scan_args *args, void *stream);
 
+/* A long sequence, or one of few channels, is cut into chunks that run side by side where the
+ * calling thread's workspace (conv2d_set_workspace) holds this many bytes for the chunks'
+ * states; 0: the call is not split. Without it the call gives the same results up to
+ * rounding, slower. Host only. */
+int selective_scan_workspace_size(const selective_scan_args *args, size_t *bytes);
+
 /* The same for one token of each of nseq sequences, as causal_conv1d_step. */
 int selective_scan_step(const selective_scan_args *args, void *stream);
 

@@ -478,3 +478,64 @@ def test_binding_refuses():
         with pytest.raises(c2d.Conv2dError) as e:
             call()
         assert e.value.code == c2d.EINVAL
+
+
+def _long_scan(lengths, d=64, n=16, packed=True, kind="f32", groups=1):
+    c = _scan_case(31, kind, lengths, d, n, groups, {})
+    return c, _scan_args(c, lengths, packed, {})
+
+
+def _workspace_of(args, kw, lengths, packed, **more):
+    """What the library wants for a call, from the struct that the binding would pass."""
+    import ctypes
+    from conv2d_bias_activation_amd import sequence
+    taken = []
+    real = sequence._call
+    sequence._call = lambda name, packed_args, device, stream: taken.append(packed_args)
+    try:
+        c2d.selective_scan(*args, **kw, workspace=False, **more)
+    finally:
+        sequence._call = real
+    size = ctypes.c_size_t(0)
+    assert c2d._load().selective_scan_workspace_size(taken[0], ctypes.byref(size)) == c2d.OK
+    return size.value
+
+
+@pytest.mark.parametrize("lengths,packed,n,groups", [([3000], False, 16, 1), ([2000, 1, 0, 900, 64, 65], True, 16, 1),
+                                                     ([1500, 1500], False, 64, 2), ([1024, 1023, 1025], True, 5, 1),
+                                                     ([1300], True, 130, 1)])
+def test_split_scans(lengths, packed, n, groups):
+    """Sequences cut into chunks that run side by side: the right values with the workspace, without it, and the same
+    bits again; a workspace one byte short is not written."""
+    c, (d, args, kw) = _long_scan(lengths, n=n, packed=packed, groups=groups)
+    want, bound, state, state_bound = _reference(c, lengths)
+    need = _workspace_of(args, kw, lengths, packed, longest=max(lengths))
+    assert need > 0
+    seen = []
+    for ws in (None, False, torch.empty(need, dtype=torch.uint8, device=DEV), None):
+        dev_state = _on(c["state"])
+        y = c2d.selective_scan(*args, **kw, state=dev_state, longest=max(lengths), workspace=ws)
+        ref.close(y.reshape(-1, d), want, bound, f"split {lengths}")
+        ref.close(dev_state, state, state_bound, "state")
+        seen.append((y, dev_state))
+    for y, s in seen[2:]:
+        assert torch.equal(y, seen[0][0]) and torch.equal(s, seen[0][1])
+    short = torch.full((need,), 77, dtype=torch.uint8, device=DEV)[:need - 1]
+    dev_state = _on(c["state"])
+    y = c2d.selective_scan(*args, **kw, state=dev_state, longest=max(lengths), workspace=short)
+    assert (short == 77).all() and torch.equal(y, seen[1][0]) and torch.equal(dev_state, seen[1][1])
+
+
+def test_split_scan_of_wrong_offsets_stays_in_its_workspace():
+    d, n = 64, 16
+    x = torch.randn(4000, d, device=DEV)
+    b = torch.randn(4000, 1, n, device=DEV)
+    bad = torch.tensor([900, -5, 4000, 17, 3999, 2000000000], dtype=torch.int32, device=DEV)
+    args, kw = (x, x, -torch.ones(d, n, device=DEV), b, b), {"softplus": True, "seq_offsets": bad}
+    need = _workspace_of(args, kw, None, True, longest=4000)
+    assert need > 0
+    room = torch.full((need + 512,), 77, dtype=torch.uint8, device=DEV)
+    out = torch.full((4200, d), 3.0, device=DEV)
+    c2d.selective_scan(*args, **kw, longest=4000, workspace=room[256:256 + need], out=out[100:4100])
+    assert (room[:256] == 77).all() and (room[256 + need:] == 77).all()
+    assert (out[:100] == 3).all() and (out[4100:] == 3).all()
