@@ -12,8 +12,8 @@ namespace c2d {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int kRunShift = 4, kRun = 1 << kRunShift;  // tokens of a thread
-constexpr int kBatch = 8;                            // loads a thread has in flight
+constexpr int kRun = 16;   // tokens of a thread
+constexpr int kBatch = 8;  // loads a thread has in flight
 
 template <int VEC> __device__ __forceinline__ void activate_all(int act, float *v, const float *alpha) {
     if (act == CONV2D_ACT_SILU) {
@@ -81,12 +81,12 @@ __global__ __launch_bounds__(kBlock) void causal_conv_kernel(const causal_conv1d
     const T *x = static_cast<const T *>(a.x);
     T *y = static_cast<T *>(a.y);
     if (a.offsets) {
-        if (!find_run(a.offsets, a.nseq, (int)a.tokens, kRunShift, item, &r)) return;
+        if (!find_run(a.offsets, a.nseq, (int)a.tokens, kRun, item, &r)) return;
         x += (long long)r.start * a.x_token;
         y += (long long)r.start * a.y_token;
     } else {
         r.seq = item / runs;
-        r.first = (item - r.seq * runs) << kRunShift;
+        r.first = (item - r.seq * runs) * kRun;
         r.len = (int)a.tokens;
         x += (long long)r.seq * a.x_batch;
         y += (long long)r.seq * a.y_batch;
@@ -179,7 +179,7 @@ template <typename T, int VEC, int W> hipError_t launch_w(const causal_conv1d_ar
     const int tx = nvec <= 64 ? 64 : nvec <= 128 ? 128 : kBlock;  // whole waves share a run
     const int cblocks = (nvec + tx - 1) / tx;
     const int runs = (int)((a.tokens + kRun - 1) / kRun);
-    const long long items = a.offsets ? (a.tokens >> kRunShift) + a.nseq : (long long)(runs ? runs : 1) * a.nseq;
+    const long long items = a.offsets ? a.tokens / kRun + a.nseq : (long long)(runs ? runs : 1) * a.nseq;
     const long long blocks = (items + kBlock / tx - 1) / (kBlock / tx) * cblocks;
     return launch_kernel(causal_conv_kernel<T, VEC, W>, dim3((unsigned)blocks), dim3(kBlock), 0, st, a, tx, cblocks,
                          (int)items, runs ? runs : 1);

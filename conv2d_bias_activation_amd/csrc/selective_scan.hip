@@ -1,5 +1,8 @@
 // Selective state space scan over channel-last token rows, for prompts and single tokens.
+#include <algorithm>
+
 #include "kernels.hpp"
+#include "runtime.hpp"
 #include "seq_common.hpp"
 
 namespace c2d {
@@ -24,7 +27,7 @@ __device__ __forceinline__ float softplus(float x) {
 
 // What a launch adds to the arguments: how the work is cut.
 struct ScanCut {
-    int shift;    // chunks of 1 << shift tokens
+    int run;      // tokens of a chunk
     int items;    // chunk numbers in all (find_run), or nseq * chunks
     int chunks;   // unpacked: chunks of a sequence
     int cblocks;  // 64-channel blocks of a group
@@ -40,6 +43,25 @@ __device__ __forceinline__ float *record(const selective_scan_args &a, const Sca
     return k.ws + (long long)item * (a.states + 1) * a.channels;
 }
 
+constexpr int kMaxRanked = 256;  // sequences; more of them even out by themselves
+
+// The sequence that stands at place `rank` when the longest come first (ties by number), so
+// that the workgroups that start last are short.
+__device__ __forceinline__ int by_length(const int *offsets, int nseq, int tokens, int rank, int &found) {
+    for (int i = threadIdx.x; i < nseq; i += blockDim.x) {
+        const int len = clamped_offset(offsets, i + 1, tokens) - clamped_offset(offsets, i, tokens);
+        int before = 0, prev = clamped_offset(offsets, 0, tokens);
+        for (int j = 0; j < nseq; j++) {
+            const int next = clamped_offset(offsets, j + 1, tokens), other = next - prev;
+            before += other > len || (other == len && j < i);
+            prev = next;
+        }
+        if (before == rank) found = i;
+    }
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(found);
+}
+
 // A workgroup takes 64 channels (one a lane) of one chunk of a sequence. Its NW waves share the
 // states of those channels, NS a lane, so that few channels still make many waves, and walk
 // the chunk in tiles of TT tokens:
@@ -52,11 +74,12 @@ __device__ __forceinline__ float *record(const selective_scan_args &a, const Sca
 // Bound by the vector ALU: 6 N issue slots a token and channel and about 36 for the step
 // size, gate and conversions, against 4 values moved.
 template <typename T, int NS, int NW, bool FIRST>
-__global__ __launch_bounds__(64 * NW) void scan_prompt_kernel(const selective_scan_args a, const ScanCut k) {
-    constexpr int TT = NW == 16 ? 8 : 16;
+__global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW == 2 ? 5 : NW <= 8 ? 6 : NS == 4 ? 8 : 4) void scan_prompt_kernel(const selective_scan_args a, const ScanCut k) {
+    constexpr int TT = NW == 16 || NW <= 2 ? 8 : 16;
     constexpr int NP = NS * NW;                  // states with their padding
     constexpr int EPT = (TT + NW - 1) / NW;      // tile tokens of a thread
     constexpr int BCE = TT * NP * 2 / (64 * NW);  // b and c values of a thread
+    __shared__ int s_seq;
     __shared__ float2 s_d[TT][64];               // d, d * u
     __shared__ __attribute__((aligned(16))) float s_bc[2][TT][NP];
     __shared__ float s_y[FIRST ? 1 : NW][FIRST ? 1 : TT][64];
@@ -72,23 +95,33 @@ __global__ __launch_bounds__(64 * NW) void scan_prompt_kernel(const selective_sc
     SeqRun r;
     long long start = 0;
     if (a.offsets) {
-        if (!find_run(a.offsets, a.nseq, (int)a.tokens, k.shift, item, &r)) return;
+        if (!k.ws && a.nseq <= kMaxRanked) {
+            const int s = by_length(a.offsets, a.nseq, (int)a.tokens, item, s_seq);
+            r.seq = s;
+            r.start = clamped_offset(a.offsets, s, (int)a.tokens);
+            const int e = clamped_offset(a.offsets, s + 1, (int)a.tokens);
+            r.len = e > r.start ? e - r.start : 0;
+            r.first = 0;
+        } else if (!find_run(a.offsets, a.nseq, (int)a.tokens, k.run, item, &r)) {
+            return;
+        }
         start = r.start;
     } else {
         r.seq = item / k.chunks;
-        r.first = (item - r.seq * k.chunks) << k.shift;
+        r.first = (item - r.seq * k.chunks) * k.run;
         r.len = (int)a.tokens;
     }
-    const int chunk = r.first >> k.shift;
-    const int last = r.len > 0 ? (r.len - 1) >> k.shift : 0;
+    const int chunk = r.first / k.run;
+    const int last = r.len > 0 ? (r.len - 1) / k.run : 0;
     if (FIRST && chunk == last) return;
     const long long lead = a.offsets ? 0 : r.seq;
-    const T *u = (const T *)a.u + lead * a.u_batch + start * a.u_token + c;
-    const T *dt = (const T *)a.dt + lead * a.dt_batch + start * a.dt_token + c;
+    const T *u = (const T *)a.u + lead * a.u_batch + start * a.u_token;
+    const T *dt = (const T *)a.dt + lead * a.dt_batch + start * a.dt_token;
     const T *bp = (const T *)a.b + lead * a.b_batch + start * a.b_token + (long long)g * a.states;
     const T *cp = (const T *)a.c + lead * a.c_batch + start * a.c_token + (long long)g * a.states;
-    const T *gate = a.gate ? (const T *)a.gate + lead * a.gate_batch + start * a.gate_token + c : nullptr;
-    T *y = (T *)a.y + lead * a.y_batch + start * a.y_token + c;
+    const bool gated = !FIRST && a.gate;
+    const T *gate = (const T *)a.gate + lead * a.gate_batch + start * a.gate_token;
+    T *y = (T *)a.y + lead * a.y_batch + start * a.y_token;
 
     const int row = state_row(a.state, a.slots, r.seq, a.state_rows);
     float *state = row < 0 ? nullptr : a.state + ((long long)row * a.channels + c) * a.states;
@@ -107,96 +140,131 @@ __global__ __launch_bounds__(64 * NW) void scan_prompt_kernel(const selective_sc
             if (on && wave * NS + i < a.states) p[(long long)(wave * NS + i) * a.channels] = h[i];
     }
     if (!FIRST && last > 0) {
-        // the start state: chunk 0's end state decayed through the chunks after it
-        const float *p = record(a, k, chunk ? item - chunk : item + last) + c;
+        // the start state: chunk 0's end state decayed through the chunks after it, kAhead
+        // records on their way at once
+        constexpr int kAhead = NS <= 4 ? 8 : 4;
+        const long long stride = (long long)(a.states + 1) * a.channels;
+        long long at[NS];
 #pragma unroll
-        for (int i = 0; i < NS; i++)
-            if (wave * NS + i < a.states) h[i] = p[(long long)(wave * NS + i + 1) * a.channels];
-#pragma unroll 4
-        for (int j = 1; j < chunk; j++) {
-            const float *q = record(a, k, item - chunk + j) + c;
-            const float sum = q[0];
+        for (int i = 0; i < NS; i++) at[i] = (long long)(min(wave * NS + i, a.states - 1) + 1) * a.channels + c;
+        const float *p = record(a, k, chunk ? item - chunk : item + last);
 #pragma unroll
-            for (int i = 0; i < NS; i++)
-                if (wave * NS + i < a.states)
-                    h[i] = fmaf(__builtin_amdgcn_exp2f(sum * A[i]), h[i], q[(long long)(wave * NS + i + 1) * a.channels]);
+        for (int i = 0; i < NS; i++) h[i] = wave * NS + i < a.states ? p[at[i]] : 0.0f;
+        for (int j = 1; j < chunk; j += kAhead) {
+            float sum[kAhead], add[kAhead][NS];
+#pragma unroll
+            for (int m = 0; m < kAhead; m++) {
+                const float *q = p + min(j + m, chunk - 1) * stride;
+                sum[m] = q[c];
+#pragma unroll
+                for (int i = 0; i < NS; i++) add[m][i] = q[at[i]];
+            }
+#pragma unroll
+            for (int m = 0; m < kAhead; m++)
+                if (j + m < chunk) {
+#pragma unroll
+                    for (int i = 0; i < NS; i++)
+                        h[i] = fmaf(__builtin_amdgcn_exp2f(sum[m] * A[i]), h[i], wave * NS + i < a.states ? add[m][i] : 0.0f);
+                }
         }
     }
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.0f, skip = a.skip ? a.skip[c] : 0.0f;
-    const int waves = (a.states + NS - 1) / NS;  // waves with states
+    const int waves = (a.states + NS - 1) / NS;  // waves with states; the others' part of y is 0
+    if (!FIRST && wave >= waves) {
+#pragma unroll
+        for (int t = 0; t < TT; t++) s_y[wave][t][lane] = 0.0f;
+    }
     float dsum = 0.0f;
 
-    const int end = r.len < r.first + (1 << k.shift) ? r.len : r.first + (1 << k.shift);
-    T nu[EPT], nd[EPT], ng[EPT], nbc[BCE];
-    auto fetch = [&](int t0) {
+    const int end = min(r.len, r.first + k.run);
+    T nu[EPT], nd[EPT], ng[EPT], nbc[BCE];  // the next tile
+    auto fetch = [&](int t0) {              // past the end: the last token again
 #pragma unroll
         for (int e = 0; e < EPT; e++) {
-            const int t = t0 + e * NW + wave;
-            if (e * NW + wave < TT && t < end) {
-                nu[e] = u[t * a.u_token];
-                nd[e] = dt[t * a.dt_token];
-                if (!FIRST && gate) ng[e] = gate[t * a.gate_token];
-            }
+            const long long t = min(t0 + e * NW + wave, end - 1);
+            nu[e] = (u + t * a.u_token)[(unsigned)c];
+            nd[e] = (dt + t * a.dt_token)[(unsigned)c];
+            if (gated) ng[e] = (gate + t * a.gate_token)[(unsigned)c];
         }
 #pragma unroll
         for (int e = 0; e < BCE; e++) {
             const int i = e * 64 * NW + threadIdx.x;
-            const int n = i % NP, t = t0 + i / NP % TT;
-            nbc[e] = (T)0.0f;
-            if (n < a.states && t < end && (!FIRST || i < TT * NP))
-                nbc[e] = (i < TT * NP ? bp + t * a.b_token : cp + t * a.c_token)[n];
+            const int n = min(i % NP, a.states - 1);
+            const long long t = min(t0 + i / NP % TT, end - 1);
+            if (i < TT * NP)
+                nbc[e] = (bp + t * a.b_token)[(unsigned)n];
+            else if (!FIRST)
+                nbc[e] = (cp + t * a.c_token)[(unsigned)n];
         }
     };
-    fetch(r.first);
-    for (int t0 = r.first; t0 < end; t0 += TT) {
-        float x[EPT], z[EPT];
+    auto tile = [&](int t0, auto full) {
+        constexpr bool kFull = decltype(full)::value;
+        float x[EPT], z[EPT], d[EPT];
+#pragma unroll
+        for (int e = 0; e < EPT; e++) {
+            x[e] = to_f32(nu[e]);
+            d[e] = to_f32(nd[e]) + bias;
+            z[e] = to_f32(ng[e]);
+        }
+        if (a.softplus) {
+#pragma unroll
+            for (int e = 0; e < EPT; e++) d[e] = softplus(d[e]);
+        }
 #pragma unroll
         for (int e = 0; e < EPT; e++) {
             const int tt = e * NW + wave;
-            if (tt < TT) {
-                const bool in = t0 + tt < end;
-                x[e] = in ? to_f32(nu[e]) : 0.0f;
-                z[e] = in && !FIRST && gate ? to_f32(ng[e]) : 0.0f;
-                float d = in ? to_f32(nd[e]) + bias : 0.0f;
-                if (a.softplus && in) d = softplus(d);
-                s_d[tt][lane] = float2{d, d * x[e]};
-            }
+            const bool in = kFull || t0 + tt < end;
+            if (tt < TT) s_d[tt][lane] = in ? float2{d[e], d[e] * x[e]} : float2{0.0f, 0.0f};
         }
 #pragma unroll
         for (int e = 0; e < BCE; e++) {
             const int i = e * 64 * NW + threadIdx.x;
-            (&s_bc[0][0][0])[i] = to_f32(nbc[e]);
+            const bool in = i % NP < a.states && (kFull || t0 + i / NP % TT < end);
+            if (!FIRST || i < TT * NP) (&s_bc[0][0][0])[i] = in ? to_f32(nbc[e]) : 0.0f;
         }
         fetch(t0 + TT);
         __syncthreads();
         if (wave < waves) {
 #pragma unroll
             for (int t = 0; t < TT; t++) {
-                const float2 d = s_d[t][lane];
-                if (FIRST) dsum += d.x;
+                const float2 v = s_d[t][lane];
+                if (FIRST) dsum += v.x;
                 float sum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < NS; i++) {
-                    const float add = d.y * s_bc[0][t][wave * NS + i];
-                    h[i] = fmaf(__builtin_amdgcn_exp2f(d.x * A[i]), h[i], add);
+                    const float add = v.y * s_bc[0][t][wave * NS + i];
+                    h[i] = fmaf(__builtin_amdgcn_exp2f(v.x * A[i]), h[i], add);
                     if (!FIRST) sum = fmaf(h[i], s_bc[1][t][wave * NS + i], sum);
                 }
                 if (!FIRST) s_y[wave][t][lane] = sum;
             }
         }
         __syncthreads();
-        if (!FIRST) {
+        if (FIRST) return;
+        float v[EPT];
 #pragma unroll
-            for (int e = 0; e < EPT; e++) {
-                const int tt = e * NW + wave;
-                if (tt < TT && t0 + tt < end) {
-                    float sum = skip * x[e];
-                    for (int w = 0; w < waves; w++) sum += s_y[w][tt][lane];
-                    if (gate) sum *= activate_c<CONV2D_ACT_SILU>(z[e], 0.0f);
-                    if (on) y[(t0 + tt) * a.y_token] = round_fp32<T>(sum);
-                }
-            }
+        for (int e = 0; e < EPT; e++) {
+            v[e] = skip * x[e];
+#pragma unroll
+            for (int w = 0; w < NW; w++)
+                if (e * NW + wave < TT) v[e] += s_y[w][e * NW + wave][lane];
         }
+        if (gated) {
+#pragma unroll
+            for (int e = 0; e < EPT; e++) v[e] *= activate_c<CONV2D_ACT_SILU>(z[e], 0.0f);
+        }
+#pragma unroll
+        for (int e = 0; e < EPT; e++) {
+            const int tt = e * NW + wave;
+            if (on && tt < TT && (kFull || t0 + tt < end))
+                (y + (t0 + tt) * a.y_token)[(unsigned)c] = round_fp32<T>(v[e]);
+        }
+    };
+    if (end > r.first) {
+        fetch(r.first);
+        int t0 = r.first;
+        for (; t0 + TT <= end; t0 += TT) tile(t0, std::true_type{});
+        if (t0 < end) tile(t0, std::false_type{});
     }
 
     if (!on || wave >= waves) return;
@@ -243,48 +311,102 @@ int waves_of(int states) {
 
 constexpr int kBlock = 256;
 
-// Lane i of a channel's `lanes` lanes holds the states i, i + lanes, ...: S of them.
-template <typename T, int S>
+// One token of each sequence. A channel's states lie on `lanes` lanes (a power of two), VEC
+// neighbouring ones a lane, so that a wave reads and writes its state as whole cache lines;
+// with VEC = 1 (unaligned rows, or states not a multiple of four) a lane takes up to S,
+// `lanes` apart. A workgroup takes the same channels of ROWS sequences: a is read once for
+// them and their states are on their way together. Bound by the state's bytes (8 a state and
+// token), or by the launch for few rows.
+template <typename T, int VEC, int S, int ROWS>
 __global__ __launch_bounds__(kBlock) void scan_token_kernel(const selective_scan_args a, int lanes, int cblocks) {
     const int cl = threadIdx.x % lanes;
     const int ch = (int)(blockIdx.x % cblocks) * (kBlock / lanes) + threadIdx.x / lanes;
-    const int c = ch < a.channels ? ch : a.channels - 1;  // idle lanes follow for the sums across lanes
-    const long long seq = blockIdx.x / cblocks;
+    const bool on = ch < a.channels;
+    const int c = on ? ch : a.channels - 1;  // idle lanes follow for the sums across lanes
     const int g = c / (a.channels / a.groups);
-    const T *b = (const T *)a.b + seq * a.b_token + (long long)g * a.states;
-    const T *cc = (const T *)a.c + seq * a.c_token + (long long)g * a.states;
-    const int row = state_row(a.state, a.slots, (int)seq, a.state_rows);
-    float *state = row < 0 ? nullptr : a.state + ((long long)row * a.channels + c) * a.states;
-    const float x = to_f32(((const T *)a.u)[seq * a.u_token + c]);
-    float d = to_f32(((const T *)a.dt)[seq * a.dt_token + c]) + (a.dt_bias ? a.dt_bias[c] : 0.0f);
-    if (a.softplus) d = softplus(d);
-    float sum = 0.0f;
+    const int first = (int)(blockIdx.x / cblocks) * ROWS;
+
+    float A[S][VEC];
+    int at[S];
+    bool has[S];
 #pragma unroll
     for (int i = 0; i < S; i++) {
-        const int n = cl + i * lanes;
-        if (n < a.states) {
-            const float A = a.a[(long long)c * a.states + n] * kLog2e;
-            float h = state && !a.fresh ? state[n] : 0.0f;
-            h = fmaf(__builtin_amdgcn_exp2f(d * A), h, d * x * to_f32(b[n]));
-            sum = fmaf(h, to_f32(cc[n]), sum);
-            if (state && ch < a.channels) state[n] = h;
+        const int n = (cl + i * lanes) * VEC;
+        has[i] = n < a.states;
+        at[i] = has[i] ? n : 0;
+        const Pack<float, VEC> v = load_pack<float, VEC>(a.a + (long long)c * a.states + at[i]);
+#pragma unroll
+        for (int j = 0; j < VEC; j++) A[i][j] = v.v[j] * kLog2e;
+    }
+    const float bias = a.dt_bias ? a.dt_bias[c] : 0.0f, skip = a.skip ? a.skip[c] : 0.0f;
+
+    float *state[ROWS];
+    Pack<float, VEC> h[ROWS][S];
+    Pack<T, VEC> b[ROWS][S], cc[ROWS][S];
+    T u[ROWS], dt[ROWS], gate[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; r++) {
+        const long long seq = min(first + r, a.nseq - 1);
+        const int row = state_row(a.state, a.slots, (int)seq, a.state_rows);
+        state[r] = row < 0 ? nullptr : a.state + ((long long)row * a.channels + c) * a.states;
+        u[r] = ((const T *)a.u)[seq * a.u_token + c];
+        dt[r] = ((const T *)a.dt)[seq * a.dt_token + c];
+        if (a.gate) gate[r] = ((const T *)a.gate)[seq * a.gate_token + c];
+#pragma unroll
+        for (int i = 0; i < S; i++) {
+            b[r][i] = load_pack<T, VEC>((const T *)a.b + seq * a.b_token + (long long)g * a.states + at[i]);
+            cc[r][i] = load_pack<T, VEC>((const T *)a.c + seq * a.c_token + (long long)g * a.states + at[i]);
+            h[r][i] = Pack<float, VEC>{};
+            if (state[r] && !a.fresh) h[r][i] = load_pack<float, VEC>(state[r] + at[i]);
         }
     }
-    for (int o = 1; o < lanes; o *= 2) sum += __shfl_xor(sum, o);
-    if (cl != 0 || ch >= a.channels) return;
-    if (a.skip) sum = fmaf(a.skip[c], x, sum);
-    if (a.gate) sum *= activate_c<CONV2D_ACT_SILU>(to_f32(((const T *)a.gate)[seq * a.gate_token + c]), 0.0f);
-    ((T *)a.y)[seq * a.y_token + c] = round_fp32<T>(sum);
+#pragma unroll
+    for (int r = 0; r < ROWS; r++) {
+        if (first + r >= a.nseq) break;
+        const float x = to_f32(u[r]);
+        float d = to_f32(dt[r]) + bias;
+        if (a.softplus) d = softplus(d);
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < S; i++) {
+            if (!has[i]) continue;
+#pragma unroll
+            for (int j = 0; j < VEC; j++) {
+                h[r][i].v[j] = fmaf(__builtin_amdgcn_exp2f(d * A[i][j]), h[r][i].v[j], d * x * to_f32(b[r][i].v[j]));
+                sum = fmaf(h[r][i].v[j], to_f32(cc[r][i].v[j]), sum);
+            }
+            if (state[r] && on) store_pack<float, VEC>(state[r] + at[i], h[r][i]);
+        }
+        for (int o = 1; o < lanes; o *= 2) sum += __shfl_xor(sum, o);
+        sum = fmaf(skip, x, sum);
+        if (a.gate) sum *= activate_c<CONV2D_ACT_SILU>(to_f32(gate[r]), 0.0f);
+        if (cl == 0 && on) ((T *)a.y)[(long long)(first + r) * a.y_token + c] = round_fp32<T>(sum);
+    }
+}
+
+template <typename T, int VEC, int S> hipError_t launch_token(const selective_scan_args &a, hipStream_t st) {
+    int lanes = 1;
+    while (lanes * VEC < a.states && lanes < 64) lanes *= 2;
+    const int cblocks = (a.channels + kBlock / lanes - 1) / (kBlock / lanes);
+    const long long blocks = (long long)cblocks * a.nseq;
+    // two sequences a workgroup where that leaves the card full (512 sequences x 4096 channels x
+    // 16 states: 59.4 us, 4.8 TB/s; one: 63.1, four: 59.9, eight: 71.0), else one
+    if (S == 1 && blocks >= 4096)
+        return launch_kernel(scan_token_kernel<T, VEC, S, 2>, dim3((unsigned)(cblocks * ((a.nseq + 1ll) / 2))),
+                             dim3(kBlock), 0, st, a, lanes, cblocks);
+    return launch_kernel(scan_token_kernel<T, VEC, S, 1>, dim3((unsigned)blocks), dim3(kBlock), 0, st, a, lanes, cblocks);
 }
 
 template <typename T> hipError_t launch_token_t(const selective_scan_args &a, hipStream_t st) {
-    int lanes = 1;
-    while (lanes < a.states && lanes < 64) lanes *= 2;
-    const int cblocks = (a.channels + kBlock / lanes - 1) / (kBlock / lanes);
-    const dim3 grid((unsigned)((long long)cblocks * a.nseq));
-    if (a.states <= 64) return launch_kernel(scan_token_kernel<T, 1>, grid, dim3(kBlock), 0, st, a, lanes, cblocks);
-    return launch_kernel(scan_token_kernel<T, 4>, grid, dim3(kBlock), 0, st, a, lanes, cblocks);
+    const bool vec = a.states % 4 == 0 && a.b_token % 4 == 0 && a.c_token % 4 == 0 && aligned16(a.a) && aligned16(a.state) &&
+                     (uintptr_t)a.b % (4 * sizeof(T)) == 0 && (uintptr_t)a.c % (4 * sizeof(T)) == 0;
+    if (vec) return launch_token<T, 4, 1>(a, st);
+    if (a.states <= 64) return launch_token<T, 1, 1>(a, st);
+    return launch_token<T, 1, 4>(a, st);
 }
+
+constexpr int kWhole = 1 << 30;  // run of a call that is not split
+constexpr int kMaxChunks = 96;
 
 // How a prompt call is cut for a workspace of ws_bytes. A sequence left whole is walked by
 // one workgroup for each 64 channels, so its length is a time; a split one is read twice (the
@@ -298,23 +420,23 @@ ScanCut cut_prompt(const selective_scan_args &a, size_t ws_bytes, size_t *want) 
     const long long mean = total / a.nseq;
     long long longest = a.offsets ? (a.longest ? a.longest : 2 * mean) : a.tokens;
     if (longest > a.tokens) longest = a.tokens;
-    k.shift = 30;
+    k.run = kWhole;
     // tokens a wave walks one after the other, whole and split over 1024 SIMDs
-    const long long whole = longest, even = total * waves / 1024;
-    if (longest > 256 && whole > even * 18 / 10 + 128) {
-        int shift = 6;
-        while ((total >> shift) * waves > 4096 || (longest >> shift) >= 64) shift++;
-        if ((longest >> shift) >= 1) {
-            const long long items = a.offsets ? (a.tokens >> shift) + a.nseq
-                                              : ((a.tokens + (1ll << shift) - 1) >> shift) * a.nseq;
-            const size_t need = (size_t)items * (a.states + 1) * a.channels * sizeof(float);
-            *want = need;
-            if (need <= ws_bytes) k.shift = shift;
+    const long long even = total * waves / 1024;
+    if (longest > 48 && longest > even * 18 / 10 + 24) {
+        // six waves a SIMD are resident, and a chunk reads the records of those before it: whole
+        // tiles, two at least where there would be over 32 chunks (1000 tokens x 512 channels:
+        // 24.4 us in chunks of 16, 21.5 of 32; 400 tokens: 17.0 and 19.0)
+        const long long least = longest > 512 ? 16 : 0;
+        const long long run = std::max({total * waves / (6 * 1024), longest / kMaxChunks, least}) / 16 * 16 + 16;
+        if (run < longest) {
+            const long long items = a.offsets ? a.tokens / run + a.nseq : (a.tokens + run - 1) / run * a.nseq;
+            *want = (size_t)items * (a.states + 1) * a.channels * sizeof(float);
+            if (*want <= ws_bytes) k.run = (int)run;
         }
     }
-    k.chunks = a.offsets ? 0 : (int)((a.tokens + (1ll << k.shift) - 1) >> k.shift);
-    if (!a.offsets && k.chunks == 0) k.chunks = 1;  // empty sequences still have a state
-    k.items = a.offsets ? (int)((a.tokens >> k.shift) + a.nseq) : k.chunks * a.nseq;
+    k.chunks = a.offsets ? 0 : (int)std::max((a.tokens + k.run - 1) / k.run, 1ll);  // empty sequences have a state
+    k.items = a.offsets ? (int)(a.tokens / k.run + a.nseq) : k.chunks * a.nseq;
     return k;
 }
 
@@ -329,7 +451,7 @@ size_t scan_workspace(const selective_scan_args &a) {
 hipError_t launch_scan(const selective_scan_args &a, void *ws, size_t ws_bytes, hipStream_t st) {
     size_t want = 0;
     ScanCut k = cut_prompt(a, ws ? ws_bytes : 0, &want);
-    k.ws = k.shift < 30 ? static_cast<float *>(ws) : nullptr;
+    k.ws = k.run < kWhole ? static_cast<float *>(ws) : nullptr;
     switch (a.dtype) {
     case CONV2D_DTYPE_F32:
         return launch_prompt_t<float>(a, k, st);

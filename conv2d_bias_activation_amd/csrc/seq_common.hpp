@@ -20,7 +20,7 @@ template <typename T, int VEC> __device__ __forceinline__ void store_pack(T *p, 
     *reinterpret_cast<Pack<T, VEC> *>(p) = v;
 }
 
-// One run of at most `1 << shift` tokens of one sequence.
+// One run of at most `run` tokens of one sequence.
 struct SeqRun {
     int seq;
     int start;  // first token row of the sequence (packed), or 0
@@ -38,18 +38,18 @@ __device__ __forceinline__ int clamped_offset(const int *offsets, int i, int tok
 // least one, and tokens / run + nseq in all, which the host knows without reading the
 // offsets. False for a number that no tokens belong to; the first run of an empty sequence
 // counts, for its state.
-__device__ __forceinline__ bool find_run(const int *offsets, int nseq, int tokens, int shift, int item, SeqRun *r) {
+__device__ __forceinline__ bool find_run(const int *offsets, int nseq, int tokens, int run, int item, SeqRun *r) {
     int lo = 0, hi = nseq - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if ((clamped_offset(offsets, mid, tokens) >> shift) + mid <= item)
+        if (clamped_offset(offsets, mid, tokens) / run + mid <= item)
             lo = mid;
         else
             hi = mid - 1;
     }
     const int start = clamped_offset(offsets, lo, tokens);
     const int end = clamped_offset(offsets, lo + 1, tokens);
-    const long long first = (long long)(item - (start >> shift) - lo) << shift;
+    const long long first = (long long)(item - start / run - lo) * run;
     r->seq = lo;
     r->start = start;
     r->len = end > start ? end - start : 0;
