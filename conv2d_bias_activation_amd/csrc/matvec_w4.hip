@@ -29,14 +29,14 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(const uint8_t *codes, cons
         const long long tile = i / 256;
         const int n = (int)(tile / kb) * kTileN + l % 16;
         const int k0 = (int)(tile % kb) * kTileK + 32 * j + 8 * (l / 16);
-        uint32_t w = 0;
-        for (int e = 0; e < 8; e++) {
-            const int k = k0 + e;
-            if (n < N && k < K) {
-                const uint32_t q = codes[(long long)n * bytes + k / 2] >> (4 * (k % 2)) & 15u;
-                w |= q << (16 * (e % 2) + 4 * (e / 2));
-            }
+        uint32_t q = 0;  // the codes in the order of their inputs
+        if (n < N && k0 + 8 <= K) {
+            __builtin_memcpy(&q, codes + (long long)n * bytes + k0 / 2, 4);
+        } else if (n < N) {
+            for (int e = 0; k0 + e < K; e++) q |= (codes[(long long)n * bytes + (k0 + e) / 2] >> (4 * (e % 2)) & 15u) << 4 * e;
         }
+        uint32_t w = 0;
+        for (int e = 0; e < 8; e++) w |= (q >> 4 * e & 15u) << (16 * (e % 2) + 4 * (e / 2));
         packed[i] = w;
     }
     for (long long i = blockIdx.x * 256ll + threadIdx.x; i < nscale; i += gridDim.x * 256ll) {
@@ -49,51 +49,189 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(const uint8_t *codes, cons
     }
 }
 
-// One wave for 16 outputs of one row: each lane sums its record's inputs.
-template <typename T>
-__global__ __launch_bounds__(64) void matvec_w4_kernel(const matvec_w4_args a, const uint32_t *packed, const T *scales,
-                                                       const uint8_t *zeros) {
-    const int kb = (a.in_features + kTileK - 1) / kTileK, per = kTileK / a.group;
-    const int l = threadIdx.x, tiles = (a.out_features + kTileN - 1) / kTileN;
-    const int tile = blockIdx.x % tiles, r = blockIdx.x / tiles;
-    const int n = tile * kTileN + l % 16;
-    const T *x = static_cast<const T *>(a.x) + r * a.x_row;
-    float sum = 0.0f;
-    for (int b = 0; b < kb; b++) {
-        const long long at = (long long)tile * kb + b;
-        for (int j = 0; j < 4; j++) {
-            const uint32_t w = packed[at * 256 + l * 4 + j];
-            const long long g = (at * kTileN + l % 16) * per + 32 * j / a.group;
-            const float s = to_f32(scales[g]), z = zeros ? (float)zeros[g] : 8.0f;
-            float part = 0.0f;
-            for (int e = 0; e < 8; e++) {
-                const int k = b * kTileK + 32 * j + 8 * (l / 16) + e;
-                const float q = (float)(w >> (16 * (e % 2) + 4 * (e / 2)) & 15u);
-                if (k < a.in_features) part = fmaf(to_f32(x[k]), q - z, part);
-            }
-            sum = fmaf(part, s, sum);
+template <typename T> struct Frag;
+template <> struct Frag<bf16> {
+    typedef bf16 v8 __attribute__((ext_vector_type(8)));
+    static constexpr uint32_t kOnes = 0x3f803f80u;
+    // 16 + q for the codes of pair p: q in the upper four mantissa bits of 16.0
+    static __device__ __forceinline__ uint32_t pair(uint32_t w, int p) {
+        return ((p == 0 ? w << 3 : w >> (4 * p - 3)) & 0x00780078u) | 0x41804180u;
+    }
+    static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+    }
+};
+template <> struct Frag<f16> {
+    typedef f16 v8 __attribute__((ext_vector_type(8)));
+    static constexpr uint32_t kOnes = 0x3c003c00u;
+    static __device__ __forceinline__ uint32_t pair(uint32_t w, int p) {
+        return ((p < 2 ? w << (6 - 4 * p) : w >> (4 * p - 6)) & 0x03c003c0u) | 0x4c004c00u;
+    }
+    static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+    }
+};
+
+// Eight values of a row from k on, zeros from K on; rows need not be aligned.
+template <typename T> __device__ __forceinline__ u32x4 load_row8(const T *row, int k, int K) {
+    u32x4 v = {0, 0, 0, 0};
+    if (k + 8 <= K) {
+        __builtin_memcpy(&v, row + k, 16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const uint32_t h = k + e < K ? __builtin_bit_cast(uint16_t, row[k + e]) : 0;
+            v[e / 2] |= h << (16 * (e % 2));
         }
     }
-    sum += __shfl_xor(sum, 16);
-    sum += __shfl_xor(sum, 32);
-    if (l >= 16 || n >= a.out_features) return;
-    const float res = a.residual ? to_f32(static_cast<const T *>(a.residual)[r * a.residual_row + n]) : 0.0f;
+    return v;
+}
+
+// What a wave needs of one input block.
+template <int NT, int MT, int PER> struct Block {
+    u32x4 codes[NT], x[MT][4];
+    Pack<uint16_t, PER> scale[NT];
+    Pack<uint8_t, PER> zero[NT];
+};
+
+// A workgroup computes 16 NT outputs of 16 MT rows; its W waves take the input blocks in
+// turn, so that together they read whole runs of packed weights, and add up in LDS at the
+// end, in a fixed order.
+//
+// The matrix cores take x as the A operand and the codes, as the exact 16-bit values 16 + q, as
+// B: two instructions for two codes, and no multiplication with scales before the sum. With S
+// the sum of the same inputs (x times ones), a group's part of an output is
+// scale * (sum of x (16 + q) - (16 + zero) S), in fp32; the offset costs a factor of about
+// five in the sums' rounding error, which stays under 1e-6 of the output. Bound by the bytes
+// of the packed weights.
+template <typename T, int NT, int MT, int W, int PER>
+__global__ __launch_bounds__(64 * W) void matvec_w4_kernel(const matvec_w4_args a, const u32x4 *packed, const uint16_t *scales,
+                                                           const uint8_t *zeros, int nblocks) {
+    __shared__ f32x4 s_sum[W][NT * MT][64];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int KB = (a.in_features + kTileK - 1) / kTileK, tiles = (a.out_features + kTileN - 1) / kTileN;
+    const int tile0 = (int)(blockIdx.x % nblocks) * NT, row0 = (int)(blockIdx.x / nblocks) * 16 * MT;
+
+    const T *row[MT];  // the lane's rows of x (past the last one: that again, never stored)
+#pragma unroll
+    for (int m = 0; m < MT; m++)
+        row[m] = static_cast<const T *>(a.x) + min(row0 + 16 * m + lane % 16, a.rows - 1) * a.x_row;
+    long long at[NT];  // first input block of the lane's tiles
+#pragma unroll
+    for (int n = 0; n < NT; n++) at[n] = (long long)min(tile0 + n, tiles - 1) * KB;
+
+    auto load = [&](int kb, Block<NT, MT, PER> &b) {
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            b.codes[n] = packed[(at[n] + kb) * 64 + lane];
+            const long long g = ((at[n] + kb) * kTileN + lane % 16) * PER;
+            b.scale[n] = load_pack<uint16_t, PER>(scales + g);
+            if (zeros) b.zero[n] = load_pack<uint8_t, PER>(zeros + g);
+        }
+        const int k = kb * kTileK + lane / 16 * 8;
+        if ((kb + 1) * kTileK <= a.in_features) {
+#pragma unroll
+            for (int m = 0; m < MT; m++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) __builtin_memcpy(&b.x[m][j], row[m] + k + 32 * j, 16);
+        } else {
+#pragma unroll
+            for (int m = 0; m < MT; m++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) b.x[m][j] = load_row8(row[m], k + 32 * j, a.in_features);
+        }
+    };
+
+    f32x4 out[NT][MT] = {};
+    const u32x4 ones = {Frag<T>::kOnes, Frag<T>::kOnes, Frag<T>::kOnes, Frag<T>::kOnes};
+    auto multiply = [&](const Block<NT, MT, PER> &b) {
+#pragma unroll
+        for (int g = 0; g < PER; g++) {
+            f32x4 acc[NT][MT] = {}, sum[MT] = {};
+#pragma unroll
+            for (int j = g * 4 / PER; j < (g + 1) * 4 / PER; j++) {
+#pragma unroll
+                for (int m = 0; m < MT; m++) sum[m] = Frag<T>::mfma(b.x[m][j], ones, sum[m]);
+#pragma unroll
+                for (int n = 0; n < NT; n++) {
+                    u32x4 q;
+#pragma unroll
+                    for (int p = 0; p < 4; p++) q[p] = Frag<T>::pair(b.codes[n][j], p);
+#pragma unroll
+                    for (int m = 0; m < MT; m++) acc[n][m] = Frag<T>::mfma(b.x[m][j], q, acc[n][m]);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+                const float s = to_f32(__builtin_bit_cast(T, b.scale[n].v[g]));
+                const float z = zeros ? -16.0f - (float)b.zero[n].v[g] : -24.0f;
+#pragma unroll
+                for (int m = 0; m < MT; m++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        out[n][m][i] = fmaf(s, fmaf(z, sum[m][i], acc[n][m][i]), out[n][m][i]);
+            }
+        }
+    };
+    if (wave < KB) {
+        Block<NT, MT, PER> now, next;
+        load(wave, now);
+        for (int kb = wave; kb < KB; kb += W) {
+            load(min(kb + W, KB - 1), next);
+            multiply(now);
+            now = next;
+        }
+    }
+
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int m = 0; m < MT; m++) s_sum[wave][n * MT + m][lane] = out[n][m];
+    __syncthreads();
     const int act = a.act & 0xff;
-    const float v = epilogue(sum, a.bias ? a.bias[n] : 0.0f, act == CONV2D_ACT_PRELU ? a.alpha[n] : 0.0f, res,
-                             a.residual != nullptr, act, (a.act & CONV2D_RES_BEFORE_ACT) != 0);
-    static_cast<T *>(a.y)[r * a.y_row + n] = round_fp32<T>(v);
+    for (int i = threadIdx.x; i < NT * MT * 256; i += 64 * W) {
+        // value r of lane l of tile (n, m): row 4 (l / 16) + r, output l % 16
+        const int l = i % 64, r = i / 64 % 4, t = i / 256;
+        const int m = row0 + 16 * (t % MT) + l / 16 * 4 + r, n = (tile0 + t / MT) * kTileN + l % 16;
+        if (m >= a.rows || n >= a.out_features) continue;
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; w++) sum += s_sum[w][t][l][r];
+        const float res = a.residual ? to_f32(static_cast<const T *>(a.residual)[m * a.residual_row + n]) : 0.0f;
+        const float v = epilogue(sum, a.bias ? a.bias[n] : 0.0f, act == CONV2D_ACT_PRELU ? a.alpha[n] : 0.0f, res,
+                                 a.residual != nullptr, act, (a.act & CONV2D_RES_BEFORE_ACT) != 0);
+        static_cast<T *>(a.y)[m * a.y_row + n] = round_fp32<T>(v);
+    }
 }
 
 long long tiles(int N, int K) { return (long long)((N + kTileN - 1) / kTileN) * ((K + kTileK - 1) / kTileK); }
 
-template <typename T> hipError_t launch_t(const matvec_w4_args &a, hipStream_t st) {
+template <typename T, int NT, int MT, int W, int PER> hipError_t launch(const matvec_w4_args &a, hipStream_t st) {
     const long long nt = tiles(a.out_features, a.in_features);
     const char *p = static_cast<const char *>(a.packed);
-    const T *scales = reinterpret_cast<const T *>(p + nt * kTileBytes);
-    const uint8_t *zeros = reinterpret_cast<const uint8_t *>(scales + nt * kTileN * (kTileK / a.group));
-    return launch_kernel(matvec_w4_kernel<T>, dim3((unsigned)((long long)((a.out_features + kTileN - 1) / kTileN) * a.rows)),
-                         dim3(64), 0, st, a, static_cast<const uint32_t *>(a.packed), scales,
-                         a.has_zeros ? zeros : nullptr);
+    const uint16_t *scales = reinterpret_cast<const uint16_t *>(p + nt * kTileBytes);
+    const uint8_t *zeros = reinterpret_cast<const uint8_t *>(scales + nt * kTileN * PER);
+    const int nblocks = ((a.out_features + kTileN - 1) / kTileN + NT - 1) / NT;
+    const long long mblocks = (a.rows + 16 * MT - 1) / (16 * MT);
+    return launch_kernel(matvec_w4_kernel<T, NT, MT, W, PER>, dim3((unsigned)(nblocks * mblocks)), dim3(64 * W), 0, st, a,
+                         static_cast<const u32x4 *>(a.packed), scales, a.has_zeros ? zeros : nullptr, nblocks);
+}
+
+template <typename T, int PER> hipError_t launch_per(const matvec_w4_args &a, hipStream_t st) {
+    const int n = (a.out_features + kTileN - 1) / kTileN;
+    if (a.rows > 32) return launch<T, 2, 4, 4, PER>(a, st);
+    if (a.rows > 16) return launch<T, 2, 2, 8, PER>(a, st);
+#ifndef NT4
+#define NT4 1024
+#define NT2 512
+#endif
+    if (n >= NT4) return launch<T, 4, 1, 8, PER>(a, st);
+    if (n >= NT2) return launch<T, 2, 1, 8, PER>(a, st);
+    return launch<T, 1, 1, 8, PER>(a, st);
+}
+
+template <typename T> hipError_t launch_t(const matvec_w4_args &a, hipStream_t st) {
+    return a.group == 32 ? launch_per<T, 4>(a, st) : a.group == 64 ? launch_per<T, 2>(a, st) : launch_per<T, 1>(a, st);
 }
 
 }  // namespace
