@@ -104,7 +104,7 @@ template <int NT, int MT, int PER> struct Block {
 // scale * (sum of x (16 + q) - (16 + zero) S), in fp32; the offset costs a factor of about
 // five in the sums' rounding error, which stays under 1e-6 of the output. Bound by the bytes
 // of the packed weights.
-template <typename T, int NT, int MT, int W, int PER>
+template <typename T, int NT, int MT, int W, int PER, bool ZEROS>
 __global__ __launch_bounds__(64 * W) void matvec_w4_kernel(const matvec_w4_args a, const u32x4 *packed, const uint16_t *scales,
                                                            const uint8_t *zeros, int nblocks) {
     __shared__ f32x4 s_sum[W][NT * MT][64];
@@ -126,7 +126,7 @@ __global__ __launch_bounds__(64 * W) void matvec_w4_kernel(const matvec_w4_args 
             b.codes[n] = packed[(at[n] + kb) * 64 + lane];
             const long long g = ((at[n] + kb) * kTileN + lane % 16) * PER;
             b.scale[n] = load_pack<uint16_t, PER>(scales + g);
-            if (zeros) b.zero[n] = load_pack<uint8_t, PER>(zeros + g);
+            if (ZEROS) b.zero[n] = load_pack<uint8_t, PER>(zeros + g);
         }
         const int k = kb * kTileK + lane / 16 * 8;
         if ((kb + 1) * kTileK <= a.in_features) {
@@ -164,7 +164,7 @@ __global__ __launch_bounds__(64 * W) void matvec_w4_kernel(const matvec_w4_args 
 #pragma unroll
             for (int n = 0; n < NT; n++) {
                 const float s = to_f32(__builtin_bit_cast(T, b.scale[n].v[g]));
-                const float z = zeros ? -16.0f - (float)b.zero[n].v[g] : -24.0f;
+                const float z = ZEROS ? -16.0f - (float)b.zero[n].v[g] : -24.0f;
 #pragma unroll
                 for (int m = 0; m < MT; m++)
 #pragma unroll
@@ -174,12 +174,15 @@ __global__ __launch_bounds__(64 * W) void matvec_w4_kernel(const matvec_w4_args 
         }
     };
     if (wave < KB) {
-        Block<NT, MT, PER> now, next;
-        load(wave, now);
-        for (int kb = wave; kb < KB; kb += W) {
-            load(min(kb + W, KB - 1), next);
-            multiply(now);
-            now = next;
+        // one block on its way while another is multiplied
+        Block<NT, MT, PER> ring[2];
+        load(wave, ring[0]);
+        for (int kb = wave; kb < KB; kb += 2 * W) {
+            load(min(kb + W, KB - 1), ring[1]);
+            multiply(ring[0]);
+            if (kb + W >= KB) break;
+            load(min(kb + 2 * W, KB - 1), ring[0]);
+            multiply(ring[1]);
         }
     }
 
@@ -206,32 +209,46 @@ __global__ __launch_bounds__(64 * W) void matvec_w4_kernel(const matvec_w4_args 
 
 long long tiles(int N, int K) { return (long long)((N + kTileN - 1) / kTileN) * ((K + kTileK - 1) / kTileK); }
 
-template <typename T, int NT, int MT, int W, int PER> hipError_t launch(const matvec_w4_args &a, hipStream_t st) {
+template <typename T, int NT, int MT, int W, int PER, bool ZEROS> hipError_t launch(const matvec_w4_args &a, hipStream_t st) {
     const long long nt = tiles(a.out_features, a.in_features);
     const char *p = static_cast<const char *>(a.packed);
     const uint16_t *scales = reinterpret_cast<const uint16_t *>(p + nt * kTileBytes);
     const uint8_t *zeros = reinterpret_cast<const uint8_t *>(scales + nt * kTileN * PER);
     const int nblocks = ((a.out_features + kTileN - 1) / kTileN + NT - 1) / NT;
     const long long mblocks = (a.rows + 16 * MT - 1) / (16 * MT);
-    return launch_kernel(matvec_w4_kernel<T, NT, MT, W, PER>, dim3((unsigned)(nblocks * mblocks)), dim3(64 * W), 0, st, a,
-                         static_cast<const u32x4 *>(a.packed), scales, a.has_zeros ? zeros : nullptr, nblocks);
+    return launch_kernel(matvec_w4_kernel<T, NT, MT, W, PER, ZEROS>, dim3((unsigned)(nblocks * mblocks)), dim3(64 * W), 0, st, a,
+                         static_cast<const u32x4 *>(a.packed), scales, zeros, nblocks);
 }
 
-template <typename T, int PER> hipError_t launch_per(const matvec_w4_args &a, hipStream_t st) {
-    const int n = (a.out_features + kTileN - 1) / kTileN;
-    if (a.rows > 32) return launch<T, 2, 4, 4, PER>(a, st);
-    if (a.rows > 16) return launch<T, 2, 2, 8, PER>(a, st);
-#ifndef NT4
-#define NT4 1024
-#define NT2 512
-#endif
-    if (n >= NT4) return launch<T, 4, 1, 8, PER>(a, st);
-    if (n >= NT2) return launch<T, 2, 1, 8, PER>(a, st);
-    return launch<T, 1, 1, 8, PER>(a, st);
+// Output tiles (NT) and waves (W) of a workgroup. More tiles read x less often, which counts
+// from some eight rows on; fewer give more workgroups; more waves halve the blocks that each
+// reads one after the other, and make the sum in LDS longer. Times in us, 1 row / 16 rows,
+// groups of 128, weights not in cache:
+//   outputs x inputs   NT=4 W=4    NT=4 W=8    NT=2 W=8    NT=1 W=16   NT=1 W=8    NT=1 W=4
+//   32768 x 8192      33.2 / 37.6 33.6 / 39.6 31.9 / 46.3 47.5 / 87.6 40.4 / 73.5 40.8 / 70.9
+//   16384 x 4096      12.4 / 13.0 10.5 / 11.5 10.3 / 14.4 14.3 / 28.5 11.4 / 22.5 10.9 / 21.0
+//    8192 x 8192      18.8 / 19.0 13.8 / 15.7 10.1 / 13.4 11.8 / 23.3 10.6 / 20.8 13.0 / 19.5
+//    4096 x 4096      10.9 / 11.5  8.1 /  9.7  5.9 /  8.3  5.1 /  8.9  5.2 /  7.9  6.8 /  8.1
+//    2048 x 8192      17.4 / 17.9 12.3 / 14.5  8.6 / 12.0  6.5 / 12.4  7.3 / 11.4 10.3 / 12.1
+//    4096 x 1024       5.1 /  5.8  4.5 /  5.6  3.4 /  4.7  3.3 /  4.6  3.1 /  4.5  3.1 /  4.0
+template <typename T, int PER, bool ZEROS> hipError_t launch_per(const matvec_w4_args &a, hipStream_t st) {
+    const int n = (a.out_features + kTileN - 1) / kTileN, kb = (a.in_features + kTileK - 1) / kTileK;
+    if (a.rows > 16) return launch<T, 2, 2, 8, PER, ZEROS>(a, st);
+    const bool many = a.rows > 8;
+    if (n >= 2048 && many) return launch<T, 4, 1, 4, PER, ZEROS>(a, st);
+    if (n >= 1024 && many) return launch<T, 4, 1, 8, PER, ZEROS>(a, st);
+    if (n >= 512) return launch<T, 2, 1, 8, PER, ZEROS>(a, st);
+    if (kb <= 8) return launch<T, 1, 1, 4, PER, ZEROS>(a, st);
+    if (kb >= 32 && !many) return launch<T, 1, 1, 16, PER, ZEROS>(a, st);
+    return launch<T, 1, 1, 8, PER, ZEROS>(a, st);
+}
+
+template <typename T, int PER> hipError_t launch_z(const matvec_w4_args &a, hipStream_t st) {
+    return a.has_zeros ? launch_per<T, PER, true>(a, st) : launch_per<T, PER, false>(a, st);
 }
 
 template <typename T> hipError_t launch_t(const matvec_w4_args &a, hipStream_t st) {
-    return a.group == 32 ? launch_per<T, 4>(a, st) : a.group == 64 ? launch_per<T, 2>(a, st) : launch_per<T, 1>(a, st);
+    return a.group == 32 ? launch_z<T, 4>(a, st) : a.group == 64 ? launch_z<T, 2>(a, st) : launch_z<T, 1>(a, st);
 }
 
 }  // namespace
