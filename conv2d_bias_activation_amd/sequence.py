@@ -18,7 +18,7 @@ import struct
 
 import torch
 
-from . import _ACTS, _DTYPES, RES_BEFORE_ACT, _check, _load, _use_workspace
+from . import _ACTS, _DTYPES, RES_BEFORE_ACT, _check, _load, _use_workspace, _ws_cache
 
 __all__ = ["causal_conv1d", "causal_conv1d_step", "selective_scan", "selective_scan_step", "w4_pack", "matvec_w4",
            "W4Weights"]
@@ -29,14 +29,13 @@ _SCAN = struct.Struct("@12P14q8i0q")
 _W4 = struct.Struct("@6P3q7i0q")
 
 
-def _stream_of(device, stream):
-    return torch.cuda.current_stream(device) if stream is None else stream
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without the object around it
 
 
 def _call(name, args, device, stream):
     """The entry point `name` on packed args, on `stream`, with the tensors' device current."""
     fn = getattr(_load(), name)
-    handle = _stream_of(device, stream).cuda_stream
+    handle = _raw_stream(device.index) if stream is None else stream.cuda_stream
     if device.index == torch.cuda.current_device():
         rc = fn(args, handle)
     else:
@@ -46,17 +45,29 @@ def _call(name, args, device, stream):
         _check(rc)
 
 
-def _empty(shape, dtype, device, stream):
+def _new(shape, dtype, device, stream):
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):  # so that the allocator reuses the memory after this stream's work
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _new_like(x, stream):
+    if stream is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
 def _scratch(device, stream, workspace, need):
-    """Registers the workspace of a call; the default one is allocated on the call's stream, so
+    """Registers the workspace of a call. The default one is allocated on the call's stream, so
     that one that has to grow is freed behind the work that still uses it."""
-    st = _stream_of(device, stream)
+    if workspace is None and device.index == torch.cuda.current_device():
+        ws = _ws_cache.get((device.index, _raw_stream(device.index) if stream is None else stream.cuda_stream))
+        if ws is not None and ws.numel() >= need:  # as below, without the detours
+            _check(_load().conv2d_set_workspace(ws.data_ptr(), ws.numel()))
+            return
+    st = torch.cuda.current_stream(device) if stream is None else stream
     with torch.cuda.stream(st):
         _use_workspace(device, st, workspace, need)
 
@@ -65,14 +76,19 @@ def _fail(name, what):
     raise ValueError(f"{name} {what}")
 
 
-def _rows(name, t, shape, dtype, device):
-    """Checks token rows (any strides but the last); their address."""
+def _refuse(name, t, shape, dtype, device):
     if t.shape != shape:
         _fail(name, f"must have shape {tuple(shape)}, has {tuple(t.shape)}")
     if t.dtype != dtype:
         _fail(name, f"has dtype {t.dtype}, expected {dtype}")
     if t.device != device:
         _fail(name, f"is on {t.device}, expected {device}")
+
+
+def _rows(name, t, shape, dtype, device):
+    """Checks token rows (any strides but the last); their address."""
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        _refuse(name, t, shape, dtype, device)
     if t.stride(-1) != 1 and t.shape[-1] > 1:
         _fail(name, "must have the values of a token contiguous")
     return t.data_ptr()
@@ -82,12 +98,8 @@ def _dense(name, t, shape, dtype, device):
     """Checks a contiguous tensor or None; its address."""
     if t is None:
         return 0
-    if t.shape != shape:
-        _fail(name, f"must have shape {tuple(shape)}, has {tuple(t.shape)}")
-    if t.dtype != dtype:
-        _fail(name, f"has dtype {t.dtype}, expected {dtype}")
-    if t.device != device:
-        _fail(name, f"is on {t.device}, expected {device}")
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        _refuse(name, t, shape, dtype, device)
     if not t.is_contiguous():
         _fail(name, "must be contiguous")
     return t.data_ptr()
@@ -117,11 +129,6 @@ def _geometry(x, seq_offsets, step, name="x"):
     return x.shape[0], x.shape[1], x.stride(0), x.stride(1)
 
 
-def _strides(t, x):
-    """Batch and token stride of token rows with as many leading dimensions as x."""
-    return (t.stride(0), t.stride(1)) if x.dim() == 3 else (0, t.stride(0))
-
-
 def _state_rows(state, shape, dtype, device):
     if state is None:
         return 0, 0
@@ -139,23 +146,23 @@ def _act(act):
 
 def _conv(name, x, w, bias, alpha, act, state, slots, fresh, seq_offsets, out, stream, step):
     dt = _storage(x)
-    dev = x.device
+    dev, dtype, shape = x.device, x.dtype, x.shape
     nseq, tokens, x_batch, x_token = _geometry(x, seq_offsets, step)
-    channels = x.shape[-1]
+    channels = shape[-1]
     if w.dim() != 2 or w.shape[0] != channels:
         _fail("w", f"must be [{channels}, width]")
     width = w.shape[1]
-    xp = _rows("x", x, x.shape, x.dtype, dev)
-    wp = _dense("w", w, w.shape, x.dtype, dev)
+    xp = _rows("x", x, shape, dtype, dev)
+    wp = _dense("w", w, w.shape, dtype, dev)
     bp = _dense("bias", bias, (channels,), torch.float32, dev)
     ap = _dense("alpha", alpha, (channels,), torch.float32, dev)
-    sp, rows = _state_rows(state, (width - 1, channels), x.dtype, dev)
+    sp, rows = _state_rows(state, (width - 1, channels), dtype, dev)
     op = _dense("seq_offsets", seq_offsets, (nseq + 1,), torch.int32, dev)
     lp = _dense("slots", slots, (nseq,), torch.int32, dev)
     if out is None:
-        out = _empty(x.shape, x.dtype, dev, stream)
-    yp = _rows("out", out, x.shape, x.dtype, dev)
-    y_batch, y_token = _strides(out, x)
+        out = _new_like(x, stream)
+    yp = _rows("out", out, shape, dtype, dev)
+    y_batch, y_token = (out.stride(0), out.stride(1)) if len(shape) == 3 else (0, out.stride(0))
     _call(name, _CONV.pack(xp, wp, bp, ap, sp, yp, op, lp, x_batch, x_token, y_batch, y_token, tokens, nseq, rows,
                            channels, width, _act(act), dt, 1 if fresh else 0), dev, stream)
     return out
@@ -184,7 +191,7 @@ def _scan(name, u, dt, A, B, C, skip, gate, dt_bias, softplus, state, slots, fre
           workspace, step):
     code = _storage(u, "u")
     dev, dtype, shape = u.device, u.dtype, u.shape
-    nseq, tokens, u_batch, u_token = _geometry(u, seq_offsets, step, "u")
+    nseq, tokens, _, u_token = _geometry(u, seq_offsets, step, "u")
     channels = shape[-1]
     if A.dim() != 2 or A.shape[0] != channels:
         _fail("A", f"must be [{channels}, states]")
@@ -197,9 +204,8 @@ def _scan(name, u, dt, A, B, C, skip, gate, dt_bias, softplus, state, slots, fre
     dp = _rows("dt", dt, shape, dtype, dev)
     bp = _rows("B", B, bc, dtype, dev)
     cp = _rows("C", C, bc, dtype, dev)
-    for n, t in (("B", B), ("C", C)):
-        if groups > 1 and t.stride(-2) != states:
-            _fail(n, "must have the groups of a token contiguous")
+    if groups > 1 and (B.stride(-2) != states or C.stride(-2) != states):
+        _fail("B and C", "must have the groups of a token contiguous")
     gp = 0 if gate is None else _rows("gate", gate, shape, dtype, dev)
     Ap = _dense("A", A, A.shape, torch.float32, dev)
     kp = _dense("skip", skip, (channels,), torch.float32, dev)
@@ -208,12 +214,16 @@ def _scan(name, u, dt, A, B, C, skip, gate, dt_bias, softplus, state, slots, fre
     op = _dense("seq_offsets", seq_offsets, (nseq + 1,), torch.int32, dev)
     lp = _dense("slots", slots, (nseq,), torch.int32, dev)
     if out is None:
-        out = _empty(shape, dtype, dev, stream)
+        out = _new_like(u, stream)
     yp = _rows("out", out, shape, dtype, dev)
-    args = _SCAN.pack(up, dp, Ap, bp, cp, kp, gp, tp, sp, yp, op, lp, u_batch, u_token, *_strides(dt, u),
-                      *_strides(B, u), *_strides(C, u), *((0, 0) if gate is None else _strides(gate, u)),
-                      *_strides(out, u), tokens, longest or 0, nseq, rows, channels, groups, states,
-                      1 if softplus else 0, code, 1 if fresh else 0)
+    if len(shape) == 3:
+        strides = (*u.stride()[:2], *dt.stride()[:2], *B.stride()[:2], *C.stride()[:2],
+                   *((0, 0) if gate is None else gate.stride()[:2]), *out.stride()[:2])
+    else:
+        strides = (0, u_token, 0, dt.stride(0), 0, B.stride(0), 0, C.stride(0), 0, 0 if gate is None else gate.stride(0),
+                   0, out.stride(0))
+    args = _SCAN.pack(up, dp, Ap, bp, cp, kp, gp, tp, sp, yp, op, lp, *strides, tokens, longest or 0, nseq, rows, channels,
+                      groups, states, 1 if softplus else 0, code, 1 if fresh else 0)
     if not step:
         need = 0
         if workspace is None:
@@ -284,9 +294,10 @@ def w4_pack(codes, scales, zeros=None, *, in_features=None, group=128, stream=No
     cp = _dense("codes", codes, (n, (k + 1) // 2), torch.uint8, scales.device)
     sp = _dense("scales", scales, (n, groups), scales.dtype, dev)
     zp = _dense("zeros", zeros, (n, groups), torch.uint8, dev)
-    data = _empty((nbytes.value,), torch.uint8, dev, stream)
+    data = _new((nbytes.value,), torch.uint8, dev, stream)
     with torch.cuda.device(dev):
-        _check(lib.matvec_w4_pack(cp, sp, zp, data.data_ptr(), n, k, group, dt, _stream_of(dev, stream).cuda_stream))
+        _check(lib.matvec_w4_pack(cp, sp, zp, data.data_ptr(), n, k, group, dt,
+                                   _raw_stream(dev.index) if stream is None else stream.cuda_stream))
     return W4Weights(data, k, n, group, zeros is not None, scales.dtype)
 
 
@@ -307,7 +318,7 @@ def matvec_w4(x, weights, bias=None, alpha=None, residual=None, *, act="none", r
     ap = _dense("alpha", alpha, (n,), torch.float32, dev)
     rp = 0 if residual is None else _rows("residual", residual, (rows, n), dtype, dev)
     if out is None:
-        out = _empty((rows, n), dtype, dev, stream)
+        out = _new((rows, n), dtype, dev, stream)
     yp = _rows("out", out, (rows, n), dtype, dev)
     _call("matvec_w4", _W4.pack(xp, weights.data.data_ptr(), bp, ap, rp, yp, x.stride(0),
                                 0 if residual is None else residual.stride(0), out.stride(0), rows,
