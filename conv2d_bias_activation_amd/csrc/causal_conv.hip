@@ -12,8 +12,6 @@ namespace c2d {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int kRun = 16;   // tokens of a thread
-constexpr int kBatch = 8;  // loads a thread has in flight
 
 template <int VEC> __device__ __forceinline__ void activate_all(int act, float *v, const float *alpha) {
     if (act == CONV2D_ACT_SILU) {
@@ -69,11 +67,14 @@ template <typename T, int VEC, int W> struct ConvWeights {
 // Block: tx threads along the channels, kBlock / tx runs. The first run of a sequence is the
 // only one that reads its state, and rewrites it from the sequence's last inputs when its own
 // outputs are done, so that the state may be updated in place.
-template <typename T, int VEC, int W>
+template <typename T, int VEC, int W, int kRun>
 __global__ __launch_bounds__(kBlock) void causal_conv_kernel(const causal_conv1d_args a, int tx, int cblocks, int items,
                                                              int runs) {
-    const int cb = blockIdx.x % cblocks;
-    const int item = __builtin_amdgcn_readfirstlane((int)(blockIdx.x / cblocks) * (kBlock / tx) + (int)threadIdx.x / tx);
+    constexpr int kBatch = kRun < 8 ? kRun : 8;  // loads a thread has in flight
+    // long runs: neighbouring runs on one XCD, whose L2 then holds the rows that both read
+    const int block = kRun == 32 ? xcd_remap(blockIdx.x, gridDim.x) : blockIdx.x;
+    const int cb = block % cblocks;
+    const int item = __builtin_amdgcn_readfirstlane((block / cblocks) * (kBlock / tx) + (int)threadIdx.x / tx);
     const int c = (cb * tx + (int)threadIdx.x % tx) * VEC;
     if (item >= items || c >= a.channels) return;
 
@@ -106,6 +107,21 @@ __global__ __launch_bounds__(kBlock) void causal_conv_kernel(const causal_conv1d
         else if (state && !a.fresh)
             past[j] = load_pack<T, VEC>(state + (long long)(W - 1 + t) * a.channels);
     }
+    // The first run of a sequence leaves the state: entry j is the input W - 1 - j places before
+    // the sequence's end, an old entry further on (j + len) where the sequence is shorter
+    // than that.
+    Pack<T, VEC> kept[W - 1];
+    if (r.first == 0 && state) {
+#pragma unroll
+        for (int j = 0; j < W - 1; j++) {
+            const int t = r.len - (W - 1) + j;
+            kept[j] = Pack<T, VEC>{};
+            if (t >= 0)
+                kept[j] = load_pack<T, VEC>(x + (long long)t * a.x_token);
+            else if (!a.fresh)
+                kept[j] = load_pack<T, VEC>(state + (long long)(W - 1 + t) * a.channels);
+        }
+    }
     ConvWeights<T, VEC, W> k;
     k.load(a, c);
 
@@ -130,17 +146,8 @@ __global__ __launch_bounds__(kBlock) void causal_conv_kernel(const causal_conv1d
     }
 
     if (r.first == 0 && state) {
-        // entry j becomes the input W - 1 - j places before the end: an old entry further on
-        // (j + len) where the sequence is shorter than that
-        for (int j = 0; j < W - 1; j++) {
-            const int t = r.len - (W - 1) + j;
-            Pack<T, VEC> v{};
-            if (t >= 0)
-                v = load_pack<T, VEC>(x + (long long)t * a.x_token);
-            else if (!a.fresh)
-                v = load_pack<T, VEC>(state + (long long)(W - 1 + t) * a.channels);
-            store_pack<T, VEC>(state + (long long)j * a.channels, v);
-        }
+#pragma unroll
+        for (int j = 0; j < W - 1; j++) store_pack<T, VEC>(state + (long long)j * a.channels, kept[j]);
     }
 }
 
@@ -169,6 +176,16 @@ __global__ __launch_bounds__(kBlock) void causal_conv_step_kernel(const causal_c
     }
 }
 
+template <typename T, int VEC, int W, int kRun> hipError_t launch_prompt(const causal_conv1d_args &a, int nvec, hipStream_t st) {
+    const int tx = nvec <= 64 ? 64 : nvec <= 128 ? 128 : kBlock;  // whole waves share a run
+    const int cblocks = (nvec + tx - 1) / tx;
+    const int runs = (int)((a.tokens + kRun - 1) / kRun);
+    const long long items = a.offsets ? a.tokens / kRun + a.nseq : (long long)(runs ? runs : 1) * a.nseq;
+    const long long blocks = (items + kBlock / tx - 1) / (kBlock / tx) * cblocks;
+    return launch_kernel(causal_conv_kernel<T, VEC, W, kRun>, dim3((unsigned)blocks), dim3(kBlock), 0, st, a, tx, cblocks,
+                         (int)items, runs ? runs : 1);
+}
+
 template <typename T, int VEC, int W> hipError_t launch_w(const causal_conv1d_args &a, bool step, hipStream_t st) {
     const int nvec = (a.channels + VEC - 1) / VEC;
     if (step) {
@@ -176,13 +193,14 @@ template <typename T, int VEC, int W> hipError_t launch_w(const causal_conv1d_ar
         return launch_kernel(causal_conv_step_kernel<T, VEC, W>, dim3((unsigned)((long long)cblocks * a.nseq)),
                              dim3(kBlock), 0, st, a, cblocks);
     }
-    const int tx = nvec <= 64 ? 64 : nvec <= 128 ? 128 : kBlock;  // whole waves share a run
-    const int cblocks = (nvec + tx - 1) / tx;
-    const int runs = (int)((a.tokens + kRun - 1) / kRun);
-    const long long items = a.offsets ? a.tokens / kRun + a.nseq : (long long)(runs ? runs : 1) * a.nseq;
-    const long long blocks = (items + kBlock / tx - 1) / (kBlock / tx) * cblocks;
-    return launch_kernel(causal_conv_kernel<T, VEC, W>, dim3((unsigned)blocks), dim3(kBlock), 0, st, a, tx, cblocks,
-                         (int)items, runs ? runs : 1);
+    // Short runs make many threads and a short walk for each; long ones read fewer rows twice
+    // and load the weights less often. Times in us of runs of 4, 16 and 32 (bf16, width 4):
+    // 77 x 512: 5.2, 9.1, -; 2000 x 1024: 6.3, 10.2, 15.0; 4000 x 4096: 23.4, 18.6, 23.4;
+    // 16384 x 2048: 46.0, 36.4, 39.2; 32768 x 4096: 177, 121, 111 (4.8 TB/s).
+    const long long vectors = (a.offsets ? a.tokens : a.tokens * a.nseq) * nvec;
+    if (vectors < 600000) return launch_prompt<T, VEC, W, 4>(a, nvec, st);
+    if (vectors < 8000000) return launch_prompt<T, VEC, W, 16>(a, nvec, st);
+    return launch_prompt<T, VEC, W, 32>(a, nvec, st);
 }
 
 template <typename T> hipError_t launch_t(const causal_conv1d_args &a, bool vec, bool step, hipStream_t st) {

@@ -139,7 +139,7 @@ int run_conv(const causal_conv1d_args *args, bool step, void *stream) {
                      a.x_token % V == 0 && a.y_token % V == 0 &&
                      (s.packed || step || (a.x_batch % V == 0 && a.y_batch % V == 0));
     // an upper bound of the workgroups of either kernel
-    if ((s.rows() / 16 + 2ll * s.nseq + 1) * (a.channels / (vec ? V : 1) / 64 + 1) >= kMaxBlocks)
+    if ((s.rows() / 4 + 2ll * s.nseq + 1) * (a.channels / (vec ? V : 1) / 64 + 1) >= kMaxBlocks)
         return too_many_blocks(op);
     const hipError_t e = launch_causal_conv(a, vec, step, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? set_ok() : hip_fail(e, op);

@@ -45,6 +45,8 @@ CONV = [  # type, lengths, packed, channels, width, act, what else
     ("bf16", [3, 20], True, 264, 4, "silu", {"state": False}),
     ("f32", [1, 0, 40], True, 129, 2, "none", {"bias": False, "fresh": True}),
     ("bf16", [2, 0, 300], True, 128, 4, "silu", {"fresh": True, "wide": 64}),
+    ("bf16", [2500, 3, 2601, 0], True, 1024, 4, "silu", {"slots": [3, 2, 1, 0]}),
+    ("f16", [8203], False, 1003, 3, "silu", {}),
 ]
 
 
@@ -99,6 +101,25 @@ def test_conv_token(kind, rows, d, width, act):
                                  slots=_on(slots))
     ref.close(got, want, bound, "conv token")
     assert torch.equal(dev_state.cpu(), state)
+
+
+def test_conv_of_a_large_batch_is_that_of_its_sequences():
+    """A batch past the size where runs grow longest has the bits of its sequences convolved one by one."""
+    d, lengths = 4096, [1000, 17, 3000, 1, 0, 5000, 2500, 4999]
+    g = torch.Generator(device=DEV).manual_seed(6)
+    x = torch.randn(sum(lengths), d, generator=g, device=DEV).bfloat16()
+    w = torch.randn(d, 4, generator=g, device=DEV).bfloat16()
+    state = torch.randn(len(lengths), 3, d, generator=g, device=DEV).bfloat16()
+    alone = state.clone()
+    y = c2d.causal_conv1d(x, w, act="silu", state=state, seq_offsets=_offsets(lengths))
+    first = 0
+    for i, n in enumerate(lengths):
+        for part in range(0, n, 1000):
+            cut = x[first + part:first + min(n, part + 1000)]
+            z = c2d.causal_conv1d(cut[None], w, act="silu", state=alone[i:i + 1])
+            assert torch.equal(z[0], y[first + part:first + part + len(cut)])
+        first += n
+    assert torch.equal(state, alone)
 
 
 # ---------------------------------------------------------------- selective scan
