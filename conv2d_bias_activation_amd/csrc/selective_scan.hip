@@ -77,8 +77,9 @@ template <typename T, int NS, int NW, bool FIRST>
 __global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW == 2 ? 5 : NW <= 8 ? 6 : NS == 4 ? 8 : 4) void scan_prompt_kernel(const selective_scan_args a, const ScanCut k) {
     constexpr int TT = NW == 16 || NW <= 2 ? 8 : 16;
     constexpr int NP = NS * NW;                  // states with their padding
-    constexpr int EPT = (TT + NW - 1) / NW;      // tile tokens of a thread
-    constexpr int BCE = TT * NP * 2 / (64 * NW);  // b and c values of a thread
+    constexpr int EPT = (TT + NW - 1) / NW;       // tile tokens of a thread
+    constexpr bool kEven = TT % NW == 0;          // all waves have as many
+    constexpr int BCE = TT * NP * 2 / (64 * NW);  // b and c values of a thread, b's first
     __shared__ int s_seq;
     __shared__ float2 s_d[TT][64];               // d, d * u
     __shared__ __attribute__((aligned(16))) float s_bc[2][TT][NP];
@@ -120,7 +121,9 @@ __global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW == 2 ? 5 : NW <= 8 ? 6 : 
     const T *bp = (const T *)a.b + lead * a.b_batch + start * a.b_token + (long long)g * a.states;
     const T *cp = (const T *)a.c + lead * a.c_batch + start * a.c_token + (long long)g * a.states;
     const bool gated = !FIRST && a.gate;
-    const T *gate = (const T *)a.gate + lead * a.gate_batch + start * a.gate_token;
+    // without a gate its loads, never used, go to u
+    const T *gate = gated ? (const T *)a.gate + lead * a.gate_batch + start * a.gate_token : u;
+    const long long gate_token = gated ? a.gate_token : a.u_token;
     T *y = (T *)a.y + lead * a.y_batch + start * a.y_token;
 
     const int row = state_row(a.state, a.slots, r.seq, a.state_rows);
@@ -178,23 +181,32 @@ __global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW == 2 ? 5 : NW <= 8 ? 6 : 
 
     const int end = min(r.len, r.first + k.run);
     T nu[EPT], nd[EPT], ng[EPT], nbc[BCE];  // the next tile
-    auto fetch = [&](int t0) {              // past the end: the last token again
+    // Offsets of its first row of this wave, and of the lane's rows of b and c: they move on by
+    // a tile with each fetch. Rows past the end are the last one again.
+    const int first = r.first + wave, past = end - 1;
+    long long ou = first * a.u_token, od = first * a.dt_token, og = first * gate_token, ob[BCE];
+#pragma unroll
+    for (int e = 0; e < BCE; e++) {
+        const int i = e * 64 * NW + threadIdx.x;
+        ob[e] = (r.first + i / NP % TT) * (i < TT * NP ? a.b_token : a.c_token);
+    }
+    auto fetch = [&](int t0) {
 #pragma unroll
         for (int e = 0; e < EPT; e++) {
-            const long long t = min(t0 + e * NW + wave, end - 1);
-            nu[e] = (u + t * a.u_token)[(unsigned)c];
-            nd[e] = (dt + t * a.dt_token)[(unsigned)c];
-            if (gated) ng[e] = (gate + t * a.gate_token)[(unsigned)c];
+            const bool in = t0 + e * NW + wave < end;
+            nu[e] = (u + (in ? ou + e * NW * a.u_token : past * a.u_token))[(unsigned)c];
+            nd[e] = (dt + (in ? od + e * NW * a.dt_token : past * a.dt_token))[(unsigned)c];
+            if (!FIRST) ng[e] = (gate + (in ? og + e * NW * gate_token : past * gate_token))[(unsigned)c];
         }
+        ou += TT * a.u_token, od += TT * a.dt_token, og += TT * gate_token;
 #pragma unroll
         for (int e = 0; e < BCE; e++) {
             const int i = e * 64 * NW + threadIdx.x;
             const int n = min(i % NP, a.states - 1);
-            const long long t = min(t0 + i / NP % TT, end - 1);
-            if (i < TT * NP)
-                nbc[e] = (bp + t * a.b_token)[(unsigned)n];
-            else if (!FIRST)
-                nbc[e] = (cp + t * a.c_token)[(unsigned)n];
+            const bool in = t0 + i / NP % TT < end;
+            const long long token = i < TT * NP ? a.b_token : a.c_token;
+            if (!FIRST || i < TT * NP) nbc[e] = ((i < TT * NP ? bp : cp) + (in ? ob[e] : past * token))[(unsigned)n];
+            ob[e] += TT * token;
         }
     };
     auto tile = [&](int t0, auto full) {
@@ -214,7 +226,7 @@ __global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW == 2 ? 5 : NW <= 8 ? 6 : 
         for (int e = 0; e < EPT; e++) {
             const int tt = e * NW + wave;
             const bool in = kFull || t0 + tt < end;
-            if (tt < TT) s_d[tt][lane] = in ? float2{d[e], d[e] * x[e]} : float2{0.0f, 0.0f};
+            if (kEven || tt < TT) s_d[tt][lane] = in ? float2{d[e], d[e] * x[e]} : float2{0.0f, 0.0f};
         }
 #pragma unroll
         for (int e = 0; e < BCE; e++) {
@@ -247,7 +259,7 @@ __global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW == 2 ? 5 : NW <= 8 ? 6 : 
             v[e] = skip * x[e];
 #pragma unroll
             for (int w = 0; w < NW; w++)
-                if (e * NW + wave < TT) v[e] += s_y[w][e * NW + wave][lane];
+                if (kEven || e * NW + wave < TT) v[e] += s_y[w][e * NW + wave][lane];
         }
         if (gated) {
 #pragma unroll
@@ -256,7 +268,7 @@ __global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW == 2 ? 5 : NW <= 8 ? 6 : 
 #pragma unroll
         for (int e = 0; e < EPT; e++) {
             const int tt = e * NW + wave;
-            if (on && tt < TT && (kFull || t0 + tt < end))
+            if (on && (kEven || tt < TT) && (kFull || t0 + tt < end))
                 (y + (t0 + tt) * a.y_token)[(unsigned)c] = round_fp32<T>(v[e]);
         }
     };
