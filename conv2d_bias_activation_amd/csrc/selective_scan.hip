@@ -31,6 +31,7 @@ struct ScanCut {
     int items;    // chunk numbers in all (find_run), or nseq * chunks
     int chunks;   // unpacked: chunks of a sequence
     int cblocks;  // 64-channel blocks of a group
+    bool vec;     // states a multiple of four, a and the state 16-byte aligned
     float *ws;    // split sequences: a record per item, see Record
 };
 
@@ -62,6 +63,21 @@ __device__ __forceinline__ int by_length(const int *offsets, int nseq, int token
     return __builtin_amdgcn_readfirstlane(found);
 }
 
+// NS states from n on of a row of `states`, zeros behind its end.
+template <int NS> __device__ __forceinline__ void load_states(const float *row, int n, int states, bool vec, float *v) {
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < NS; i += 4) {
+            const Pack<float, 4> p = n + i < states ? load_pack<float, 4>(row + n + i) : Pack<float, 4>{};
+#pragma unroll
+            for (int j = 0; j < 4; j++) v[i + j] = p.v[j];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NS; i++) v[i] = n + i < states ? row[n + i] : 0.0f;
+    }
+}
+
 // A workgroup takes 64 channels (one a lane) of one chunk of a sequence. Its NW waves share the
 // states of those channels, NS a lane, so that few channels still make many waves, and walk
 // the chunk in tiles of TT tokens:
@@ -75,7 +91,8 @@ __device__ __forceinline__ int by_length(const int *offsets, int nseq, int token
 // size, gate and conversions, against 4 values moved.
 template <typename T, int NS, int NW, bool FIRST>
 __global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW == 2 ? 5 : NW <= 8 ? 6 : NS == 4 ? 8 : 4) void scan_prompt_kernel(const selective_scan_args a, const ScanCut k) {
-    constexpr int TT = NW == 16 || NW <= 2 ? 8 : 16;
+        // tokens of a tile; eight where sixteen would leave fewer waves resident for want of LDS
+    constexpr int TT = NS * NW > 64 || NW <= 2 ? 8 : 16;
     constexpr int NP = NS * NW;                  // states with their padding
     constexpr int EPT = (TT + NW - 1) / NW;       // tile tokens of a thread
     constexpr bool kEven = TT % NW == 0;          // all waves have as many
@@ -129,12 +146,13 @@ __global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW == 2 ? 5 : NW <= 8 ? 6 : 
     const int row = state_row(a.state, a.slots, r.seq, a.state_rows);
     float *state = row < 0 ? nullptr : a.state + ((long long)row * a.channels + c) * a.states;
     float h[NS], A[NS];
+    const bool starts = chunk == 0 && (FIRST || last == 0) && state && !a.fresh;
+    load_states<NS>(a.a + (long long)c * a.states, wave * NS, a.states, k.vec, A);
+    if (starts) load_states<NS>(state, wave * NS, a.states, k.vec, h);
 #pragma unroll
     for (int i = 0; i < NS; i++) {
-        const int n = wave * NS + i;
-        A[i] = n < a.states ? a.a[(long long)c * a.states + n] * kLog2e : 0.0f;
-        h[i] = 0.0f;
-        if (n < a.states && chunk == 0 && (FIRST || last == 0) && state && !a.fresh) h[i] = state[n];
+        A[i] *= kLog2e;
+        if (!starts) h[i] = 0.0f;
     }
     if (FIRST && chunk == 0) {
         float *p = record(a, k, item + last) + a.channels + c;
@@ -287,9 +305,16 @@ __global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW == 2 ? 5 : NW <= 8 ? 6 : 
         for (int i = 0; i < NS; i++)
             if (wave * NS + i < a.states) p[(long long)(wave * NS + i + 1) * a.channels] = h[i];
     } else if (state && chunk == last) {
+        if (k.vec) {
 #pragma unroll
-        for (int i = 0; i < NS; i++)
-            if (wave * NS + i < a.states) state[wave * NS + i] = h[i];
+            for (int i = 0; i < NS; i += 4)
+                if (wave * NS + i < a.states)
+                    store_pack<float, 4>(state + wave * NS + i, Pack<float, 4>{{h[i], h[i + 1], h[i + 2], h[i + 3]}});
+        } else {
+#pragma unroll
+            for (int i = 0; i < NS; i++)
+                if (wave * NS + i < a.states) state[wave * NS + i] = h[i];
+        }
     }
 }
 
@@ -433,6 +458,7 @@ ScanCut cut_prompt(const selective_scan_args &a, size_t ws_bytes, size_t *want) 
     long long longest = a.offsets ? (a.longest ? a.longest : 2 * mean) : a.tokens;
     if (longest > a.tokens) longest = a.tokens;
     k.run = kWhole;
+    k.vec = a.states % 4 == 0 && aligned16(a.a) && aligned16(a.state);
     // tokens a wave walks one after the other, whole and split over 1024 SIMDs
     const long long even = total * waves / 1024;
     if (longest > 48 && longest > even * 18 / 10 + 24) {
