@@ -165,18 +165,18 @@ __global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW == 2 ? 5 : NW <= 8 ? 6 : 
         // records on their way at once
         constexpr int kAhead = NS <= 4 ? 8 : 4;
         const long long stride = (long long)(a.states + 1) * a.channels;
-        long long at[NS];
+        unsigned at[NS];  // states past the end take the last one's and are cleared behind
 #pragma unroll
-        for (int i = 0; i < NS; i++) at[i] = (long long)(min(wave * NS + i, a.states - 1) + 1) * a.channels + c;
+        for (int i = 0; i < NS; i++) at[i] = (unsigned)(min(wave * NS + i, a.states - 1) + 1) * a.channels + c;
         const float *p = record(a, k, chunk ? item - chunk : item + last);
 #pragma unroll
-        for (int i = 0; i < NS; i++) h[i] = wave * NS + i < a.states ? p[at[i]] : 0.0f;
+        for (int i = 0; i < NS; i++) h[i] = p[at[i]];
         for (int j = 1; j < chunk; j += kAhead) {
             float sum[kAhead], add[kAhead][NS];
 #pragma unroll
             for (int m = 0; m < kAhead; m++) {
                 const float *q = p + min(j + m, chunk - 1) * stride;
-                sum[m] = q[c];
+                sum[m] = q[(unsigned)c];
 #pragma unroll
                 for (int i = 0; i < NS; i++) add[m][i] = q[at[i]];
             }
@@ -184,10 +184,12 @@ __global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW == 2 ? 5 : NW <= 8 ? 6 : 
             for (int m = 0; m < kAhead; m++)
                 if (j + m < chunk) {
 #pragma unroll
-                    for (int i = 0; i < NS; i++)
-                        h[i] = fmaf(__builtin_amdgcn_exp2f(sum[m] * A[i]), h[i], wave * NS + i < a.states ? add[m][i] : 0.0f);
+                    for (int i = 0; i < NS; i++) h[i] = fmaf(__builtin_amdgcn_exp2f(sum[m] * A[i]), h[i], add[m][i]);
                 }
         }
+#pragma unroll
+        for (int i = 0; i < NS; i++)
+            if (wave * NS + i >= a.states) h[i] = 0.0f;
     }
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.0f, skip = a.skip ? a.skip[c] : 0.0f;
     const int waves = (a.states + NS - 1) / NS;  // waves with states; the others' part of y is 0
@@ -245,6 +247,7 @@ __global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW == 2 ? 5 : NW <= 8 ? 6 : 
             const int tt = e * NW + wave;
             const bool in = kFull || t0 + tt < end;
             if (kEven || tt < TT) s_d[tt][lane] = in ? float2{d[e], d[e] * x[e]} : float2{0.0f, 0.0f};
+            if (FIRST && in && (kEven || tt < TT)) dsum += d[e];
         }
 #pragma unroll
         for (int e = 0; e < BCE; e++) {
@@ -258,7 +261,6 @@ __global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW == 2 ? 5 : NW <= 8 ? 6 : 
 #pragma unroll
             for (int t = 0; t < TT; t++) {
                 const float2 v = s_d[t][lane];
-                if (FIRST) dsum += v.x;
                 float sum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < NS; i++) {
@@ -297,6 +299,15 @@ __global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW == 2 ? 5 : NW <= 8 ? 6 : 
         if (t0 < end) tile(t0, std::false_type{});
     }
 
+    if (FIRST) {  // the chunk's step sizes: a part in each wave
+        float *part = &s_d[0][0].x;  // free after the last tile
+        __syncthreads();
+        part[threadIdx.x] = dsum;
+        __syncthreads();
+        dsum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < NW; w++) dsum += part[w * 64 + lane];
+    }
     if (!on || wave >= waves) return;
     if (FIRST) {
         float *p = record(a, k, item) + c;
@@ -470,7 +481,8 @@ ScanCut cut_prompt(const selective_scan_args &a, size_t ws_bytes, size_t *want) 
         if (run < longest) {
             const long long items = a.offsets ? a.tokens / run + a.nseq : (a.tokens + run - 1) / run * a.nseq;
             *want = (size_t)items * (a.states + 1) * a.channels * sizeof(float);
-            if (*want <= ws_bytes) k.run = (int)run;
+            if ((a.states + 1ll) * a.channels > 1ll << 31) *want = 0;  // 32-bit offsets within a record
+            if (*want && *want <= ws_bytes) k.run = (int)run;
         }
     }
     k.chunks = a.offsets ? 0 : (int)std::max((a.tokens + k.run - 1) / k.run, 1ll);  // empty sequences have a state
