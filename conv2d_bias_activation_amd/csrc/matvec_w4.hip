@@ -72,19 +72,31 @@ template <> struct Frag<f16> {
     }
 };
 
-// Eight values of a row from k on, zeros from K on; rows need not be aligned.
+// Eight values of a row from k on, zeros from K on; rows need not be aligned. Where the eight
+// reach past the row's end its last eight are loaded and moved down.
 template <typename T> __device__ __forceinline__ u32x4 load_row8(const T *row, int k, int K) {
-    u32x4 v = {0, 0, 0, 0};
-    if (k + 8 <= K) {
-        __builtin_memcpy(&v, row + k, 16);
-    } else {
+    uint64_t lo = 0, hi = 0;
+    if (K < 8) {
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-            const uint32_t h = k + e < K ? __builtin_bit_cast(uint16_t, row[k + e]) : 0;
-            v[e / 2] |= h << (16 * (e % 2));
+        for (int e = 0; e < 7; e++) {
+            const uint64_t h = k + e < K ? __builtin_bit_cast(uint16_t, row[k + e]) : 0;
+            (e < 4 ? lo : hi) |= h << 16 * (e % 4);
+        }
+    } else {
+        const int at = min(k, K - 8), bits = 16 * min(k - at, 8);
+        u32x4 v;
+        __builtin_memcpy(&v, row + at, 16);
+        lo = (uint64_t)v[1] << 32 | v[0];
+        hi = (uint64_t)v[3] << 32 | v[2];
+        if (bits >= 64) {
+            lo = bits < 128 ? hi >> (bits - 64) : 0;
+            hi = 0;
+        } else if (bits) {
+            lo = lo >> bits | hi << (64 - bits);
+            hi >>= bits;
         }
     }
-    return v;
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
 // What a wave needs of one input block.
@@ -174,15 +186,19 @@ __global__ __launch_bounds__(64 * W) void matvec_w4_kernel(const matvec_w4_args 
         }
     };
     if (wave < KB) {
-        // one block on its way while another is multiplied
-        Block<NT, MT, PER> ring[2];
-        load(wave, ring[0]);
+        // One block on its way while another is multiplied. With four tiles, whose waves have
+        // many blocks each, loading the last one again is cheaper than a branch around it (16
+        // rows, 8192 -> 32768, groups of 64: 37.8 and 40.3 us); with fewer it is not (5 rows,
+        // 4010 -> 10007: 12.2 and 11.1 us).
+        constexpr bool kAgain = NT == 4;
+        Block<NT, MT, PER> even, odd;
+        load(wave, even);
         for (int kb = wave; kb < KB; kb += 2 * W) {
-            load(min(kb + W, KB - 1), ring[1]);
-            multiply(ring[0]);
+            if (kAgain || kb + W < KB) load(min(kb + W, KB - 1), odd);
+            multiply(even);
             if (kb + W >= KB) break;
-            load(min(kb + 2 * W, KB - 1), ring[0]);
-            multiply(ring[1]);
+            if (kAgain || kb + 2 * W < KB) load(min(kb + 2 * W, KB - 1), even);
+            multiply(odd);
         }
     }
 
