@@ -90,7 +90,7 @@ template <int NS> __device__ __forceinline__ void load_states(const float *row, 
 // Bound by the vector ALU: 6 N issue slots a token and channel and about 36 for the step
 // size, gate and conversions, against 4 values moved.
 template <typename T, int NS, int NW, bool FIRST>
-__global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW == 2 ? 5 : NW <= 8 ? 6 : NS == 4 ? 8 : 4) void scan_prompt_kernel(const selective_scan_args a, const ScanCut k) {
+__global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW <= 8 ? 5 : NS == 4 ? 8 : 4) void scan_prompt_kernel(const selective_scan_args a, const ScanCut k) {
         // tokens of a tile; eight where sixteen would leave fewer waves resident for want of LDS
     constexpr int TT = NS * NW > 64 || NW <= 2 ? 8 : 16;
     constexpr int NP = NS * NW;                  // states with their padding
@@ -163,7 +163,7 @@ __global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW == 2 ? 5 : NW <= 8 ? 6 : 
     if (!FIRST && last > 0) {
         // the start state: chunk 0's end state decayed through the chunks after it, kAhead
         // records on their way at once
-        constexpr int kAhead = NS <= 4 ? 8 : 4;
+        constexpr int kAhead = NS == 16 ? 2 : NS == 8 || NW == 8 ? 4 : 8;
         const long long stride = (long long)(a.states + 1) * a.channels;
         unsigned at[NS];  // states past the end take the last one's and are cleared behind
 #pragma unroll
@@ -473,11 +473,11 @@ ScanCut cut_prompt(const selective_scan_args &a, size_t ws_bytes, size_t *want) 
     // tokens a wave walks one after the other, whole and split over 1024 SIMDs
     const long long even = total * waves / 1024;
     if (longest > 48 && longest > even * 18 / 10 + 24) {
-        // six waves a SIMD are resident, and a chunk reads the records of those before it: whole
+        // five waves a SIMD are resident, and a chunk reads the records of those before it: whole
         // tiles, two at least where there would be over 32 chunks (1000 tokens x 512 channels:
         // 24.4 us in chunks of 16, 21.5 of 32; 400 tokens: 17.0 and 19.0)
         const long long least = longest > 512 ? 16 : 0;
-        const long long run = std::max({total * waves / (6 * 1024), longest / kMaxChunks, least}) / 16 * 16 + 16;
+        const long long run = std::max({total * waves / (5 * 1024), longest / kMaxChunks, least}) / 16 * 16 + 16;
         if (run < longest) {
             const long long items = a.offsets ? a.tokens / run + a.nseq : (a.tokens + run - 1) / run * a.nseq;
             *want = (size_t)items * (a.states + 1) * a.channels * sizeof(float);
