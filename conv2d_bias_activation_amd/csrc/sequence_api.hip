@@ -183,8 +183,8 @@ int check_scan(const selective_scan_args *args, const char *op, bool step) {
     rc = check_no_overlap(op, ey, {in[0], in[1], in[2], in[3], in[5], es, ea, ek, eb, eo, el});
     if (!rc) rc = check_no_overlap(op, es, {in[0], in[1], in[2], in[3], in[5], ea, ek, eb, eo, el});
     if (rc) return rc;
-    // an upper bound of the workgroups of either kernel (a split prompt adds at most 4096 chunks)
-    if (((long long)a.channels * (step ? a.states : 4) / 256 + a.groups + 1) * (2ll * s.nseq + 4096) >= kMaxBlocks)
+    // an upper bound of the workgroups of either kernel (a split prompt adds at most 5120 chunks)
+    if (((long long)a.channels * (step ? a.states : 4) / 256 + a.groups + 1) * (2ll * s.nseq + 5120) >= kMaxBlocks)
         return too_many_blocks(op);
     return CONV2D_OK;
 }
