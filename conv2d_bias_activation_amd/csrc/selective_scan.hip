@@ -95,10 +95,11 @@ template <int NS> __device__ __forceinline__ void load_states(const float *row, 
 // on two (the first case, at the time 273 and 396 us): more waves hide the latencies. At most
 // five waves a SIMD: registers for six spill to memory (261 us).
 template <typename T, int NS, int NW, bool FIRST>
-__global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW <= 8 ? 5 : NS == 4 ? 8 : 4) void scan_prompt_kernel(const selective_scan_args a, const ScanCut k) {
-        // tokens of a tile; eight where sixteen would leave fewer waves resident for want of LDS
+__global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW <= 8 ? 5 : NS == 4 ? 8 : 4) void scan_prompt_kernel(
+    const selective_scan_args a, const ScanCut k) {
+    // tokens of a tile; eight where sixteen would leave fewer waves resident for want of LDS
     constexpr int TT = NS * NW > 64 || NW <= 2 ? 8 : 16;
-    constexpr int NP = NS * NW;                  // states with their padding
+    constexpr int NP = NS * NW;                   // states with their padding
     constexpr int EPT = (TT + NW - 1) / NW;       // tile tokens of a thread
     constexpr bool kEven = TT % NW == 0;          // all waves have as many
     constexpr int BCE = TT * NP * 2 / (64 * NW);  // b and c values of a thread, b's first

@@ -64,6 +64,7 @@ long long rows_bytes(const Shape &s, const Rows &r) {
 
 // Whether no two rows share memory, as those of an output must not.
 bool rows_disjoint(const Shape &s, const Rows &r) {
+    if (s.rows() == 0) return true;
     if (s.step || s.packed) return s.rows() <= 1 || r.token >= r.width;
     if (s.tokens > 1 && r.token < r.width) return false;
     if (s.nseq > 1 && r.batch < r.width) return false;

@@ -29,14 +29,17 @@ _SCAN = struct.Struct("@12P14q8i0q")
 _W4 = struct.Struct("@6P3q7i0q")
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without the object around it
+# the current stream's handle and the current device, without what torch.cuda puts around them
+# (a tensor on the GPU has initialised it)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _call(name, args, device, stream):
     """The entry point `name` on packed args, on `stream`, with the tensors' device current."""
     fn = getattr(_load(), name)
     handle = _raw_stream(device.index) if stream is None else stream.cuda_stream
-    if device.index == torch.cuda.current_device():
+    if device.index == _current_device():
         rc = fn(args, handle)
     else:
         with torch.cuda.device(device):
@@ -62,7 +65,7 @@ def _new_like(x, stream):
 def _scratch(device, stream, workspace, need):
     """Registers the workspace of a call. The default one is allocated on the call's stream, so
     that one that has to grow is freed behind the work that still uses it."""
-    if workspace is None and device.index == torch.cuda.current_device():
+    if workspace is None and device.index == _current_device():
         ws = _ws_cache.get((device.index, _raw_stream(device.index) if stream is None else stream.cuda_stream))
         if ws is not None and ws.numel() >= need:  # as below, without the detours
             _check(_load().conv2d_set_workspace(ws.data_ptr(), ws.numel()))
@@ -161,8 +164,10 @@ def _conv(name, x, w, bias, alpha, act, state, slots, fresh, seq_offsets, out, s
     lp = _dense("slots", slots, (nseq,), torch.int32, dev)
     if out is None:
         out = _new_like(x, stream)
-    yp = _rows("out", out, shape, dtype, dev)
-    y_batch, y_token = (out.stride(0), out.stride(1)) if len(shape) == 3 else (0, out.stride(0))
+        yp, y_batch, y_token = out.data_ptr(), tokens * channels, channels
+    else:
+        yp = _rows("out", out, shape, dtype, dev)
+        y_batch, y_token = (out.stride(0), out.stride(1)) if len(shape) == 3 else (0, out.stride(0))
     _call(name, _CONV.pack(xp, wp, bp, ap, sp, yp, op, lp, x_batch, x_token, y_batch, y_token, tokens, nseq, rows,
                            channels, width, _act(act), dt, 1 if fresh else 0), dev, stream)
     return out
@@ -215,7 +220,9 @@ def _scan(name, u, dt, A, B, C, skip, gate, dt_bias, softplus, state, slots, fre
     lp = _dense("slots", slots, (nseq,), torch.int32, dev)
     if out is None:
         out = _new_like(u, stream)
-    yp = _rows("out", out, shape, dtype, dev)
+        yp = out.data_ptr()
+    else:
+        yp = _rows("out", out, shape, dtype, dev)
     if len(shape) == 3:
         strides = (*u.stride()[:2], *dt.stride()[:2], *B.stride()[:2], *C.stride()[:2],
                    *((0, 0) if gate is None else gate.stride()[:2]), *out.stride()[:2])
@@ -319,7 +326,9 @@ def matvec_w4(x, weights, bias=None, alpha=None, residual=None, *, act="none", r
     rp = 0 if residual is None else _rows("residual", residual, (rows, n), dtype, dev)
     if out is None:
         out = _new((rows, n), dtype, dev, stream)
-    yp = _rows("out", out, (rows, n), dtype, dev)
+        yp = out.data_ptr()
+    else:
+        yp = _rows("out", out, (rows, n), dtype, dev)
     _call("matvec_w4", _W4.pack(xp, weights.data.data_ptr(), bp, ap, rp, yp, x.stride(0),
                                 0 if residual is None else residual.stride(0), out.stride(0), rows,
                                 weights.in_features, n, weights.group, 1 if weights.zeros else 0,
