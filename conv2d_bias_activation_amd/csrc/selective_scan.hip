@@ -90,12 +90,12 @@ template <int NS> __device__ __forceinline__ void load_states(const float *row, 
 // Past the chunk's end d = d * u = 0, which keeps the states as they are.
 // Bound by the vector ALU: 6 N issue slots of four cycles a token and channel, and about 38 for
 // the step size, gate, conversions and sums, against 4 values moved. Measured, bf16, 16
-// states: 16384 ragged tokens x 4096 channels 253 us, the ALUs 93 % busy; one sequence of 32768
-// x 1024, in two passes, 231 us (85 %). Four states a lane on four waves are faster than eight
+// states: 16384 ragged tokens x 4096 channels 247 to 261 us, the ALUs 93 % busy; one sequence of
+// 32768 x 1024, in two passes, 231 to 235 us (85 %). Four states a lane on four waves are faster than eight
 // on two (the first case, at the time 273 and 396 us): more waves hide the latencies. At most
 // five waves a SIMD: registers for six spill to memory (261 us).
 template <typename T, int NS, int NW, bool FIRST>
-__global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW <= 8 ? 5 : NS == 4 ? 8 : 4) void scan_prompt_kernel(
+__global__ __launch_bounds__(64 * NW, NW <= 2 ? 4 : NW <= 8 ? 5 : NS == 4 ? 8 : 4) void scan_prompt_kernel(
     const selective_scan_args a, const ScanCut k) {
     // tokens of a tile; eight where sixteen would leave fewer waves resident for want of LDS
     constexpr int TT = NS * NW > 64 || NW <= 2 ? 8 : 16;
@@ -166,37 +166,6 @@ __global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW <= 8 ? 5 : NS == 4 ? 8 : 
         for (int i = 0; i < NS; i++)
             if (on && wave * NS + i < a.states) p[(long long)(wave * NS + i) * a.channels] = h[i];
     }
-    if (!FIRST && last > 0) {
-        // the start state: chunk 0's end state decayed through the chunks after it, kAhead
-        // records on their way at once
-        constexpr int kAhead = NS == 16 ? 2 : NS == 8 || NW == 8 ? 4 : 8;
-        const long long stride = (long long)(a.states + 1) * a.channels;
-        unsigned at[NS];  // states past the end take the last one's and are cleared behind
-#pragma unroll
-        for (int i = 0; i < NS; i++) at[i] = (unsigned)(min(wave * NS + i, a.states - 1) + 1) * a.channels + c;
-        const float *p = record(a, k, chunk ? item - chunk : item + last);
-#pragma unroll
-        for (int i = 0; i < NS; i++) h[i] = p[at[i]];
-        for (int j = 1; j < chunk; j += kAhead) {
-            float sum[kAhead], add[kAhead][NS];
-#pragma unroll
-            for (int m = 0; m < kAhead; m++) {
-                const float *q = p + min(j + m, chunk - 1) * stride;
-                sum[m] = q[(unsigned)c];
-#pragma unroll
-                for (int i = 0; i < NS; i++) add[m][i] = q[at[i]];
-            }
-#pragma unroll
-            for (int m = 0; m < kAhead; m++)
-                if (j + m < chunk) {
-#pragma unroll
-                    for (int i = 0; i < NS; i++) h[i] = fmaf(__builtin_amdgcn_exp2f(sum[m] * A[i]), h[i], add[m][i]);
-                }
-        }
-#pragma unroll
-        for (int i = 0; i < NS; i++)
-            if (wave * NS + i >= a.states) h[i] = 0.0f;
-    }
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.0f, skip = a.skip ? a.skip[c] : 0.0f;
     const int waves = (a.states + NS - 1) / NS;  // waves with states; the others' part of y is 0
     if (!FIRST && wave >= waves) {
@@ -235,6 +204,38 @@ __global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW <= 8 ? 5 : NS == 4 ? 8 : 
             ob[e] += TT * token;
         }
     };
+    if (end > r.first) fetch(r.first);  // on its way with the records
+    if (!FIRST && last > 0) {
+        // the start state: chunk 0's end state decayed through the chunks after it, kAhead
+        // records on their way at once
+        constexpr int kAhead = NS == 16 ? 2 : NS == 8 || NW == 8 ? 4 : 8;
+        const long long stride = (long long)(a.states + 1) * a.channels;
+        unsigned at[NS];  // states past the end take the last one's and are cleared behind
+#pragma unroll
+        for (int i = 0; i < NS; i++) at[i] = (unsigned)(min(wave * NS + i, a.states - 1) + 1) * a.channels + c;
+        const float *p = record(a, k, chunk ? item - chunk : item + last);
+#pragma unroll
+        for (int i = 0; i < NS; i++) h[i] = p[at[i]];
+        for (int j = 1; j < chunk; j += kAhead) {
+            float sum[kAhead], add[kAhead][NS];
+#pragma unroll
+            for (int m = 0; m < kAhead; m++) {
+                const float *q = p + min(j + m, chunk - 1) * stride;
+                sum[m] = q[(unsigned)c];
+#pragma unroll
+                for (int i = 0; i < NS; i++) add[m][i] = q[at[i]];
+            }
+#pragma unroll
+            for (int m = 0; m < kAhead; m++)
+                if (j + m < chunk) {
+#pragma unroll
+                    for (int i = 0; i < NS; i++) h[i] = fmaf(__builtin_amdgcn_exp2f(sum[m] * A[i]), h[i], add[m][i]);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < NS; i++)
+            if (wave * NS + i >= a.states) h[i] = 0.0f;
+    }
     auto tile = [&](int t0, auto full) {
         constexpr bool kFull = decltype(full)::value;
         float x[EPT], z[EPT], d[EPT];
@@ -298,12 +299,9 @@ __global__ __launch_bounds__(64 * NW, NW == 1 ? 4 : NW <= 8 ? 5 : NS == 4 ? 8 : 
                 (y + (t0 + tt) * a.y_token)[(unsigned)c] = round_fp32<T>(v[e]);
         }
     };
-    if (end > r.first) {
-        fetch(r.first);
-        int t0 = r.first;
-        for (; t0 + TT <= end; t0 += TT) tile(t0, std::true_type{});
-        if (t0 < end) tile(t0, std::false_type{});
-    }
+    int t0 = r.first;
+    for (; t0 + TT <= end; t0 += TT) tile(t0, std::true_type{});
+    if (t0 < end) tile(t0, std::false_type{});
 
     if (FIRST) {  // the chunk's step sizes: a part in each wave
         float *part = &s_d[0][0].x;  // free after the last tile
