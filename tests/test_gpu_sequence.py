@@ -199,6 +199,32 @@ def test_scan_prompt(i):
             ref.close(dev_state, state, state_bound, "state")
 
 
+def test_scan_of_many_short_sequences():
+    """More sequences than are put in order of their lengths."""
+    g = _rng(40)
+    lengths = torch.randint(0, 9, (300,), generator=g).tolist()
+    c = _scan_case(41, "f32", lengths, 64, 8, 2, {})
+    want, bound, state, state_bound = _reference(c, lengths)
+    _, args, kw = _scan_args(c, lengths, True, {})
+    dev_state = _on(c["state"])
+    ref.close(c2d.selective_scan(*args, **kw, state=dev_state), want, bound, "many")
+    ref.close(dev_state, state, state_bound, "state")
+
+
+def test_scan_token_of_a_large_batch():
+    """Past the size where a workgroup takes two sequences, an odd number of them."""
+    rows, d, n = 513, 512, 16
+    c = _scan_case(42, "bf16", [1] * rows, d, n, 1, {})
+    c["slots"] = torch.randperm(rows + 2, generator=_rng(3))[:rows].to(torch.int32)
+    c["slots"][5] = -1
+    want, bound, state, state_bound = _reference(c, [1] * rows)
+    _, args, kw = _scan_args(c, [1] * rows, True, {})
+    del kw["seq_offsets"]
+    dev_state = _on(c["state"])
+    ref.close(c2d.selective_scan_step(*args, **kw, state=dev_state), want, bound, "large batch")
+    ref.close(dev_state, state, state_bound, "state")
+
+
 @pytest.mark.parametrize("kind", list(TYPES))
 @pytest.mark.parametrize("rows,d,n,groups", [(1, 1, 1, 1), (1, 2048, 16, 1), (7, 96, 64, 8), (5, 70, 5, 2), (3, 33, 256, 1),
                                              (2, 260, 130, 1)])
@@ -283,6 +309,12 @@ W4 = [  # type, rows, in, out, group, zeros, act, residual, before, what else
     ("bf16", 70, 72, 31, 32, False, "silu", False, False, {}),
     ("f16", 8, 4100, 1030, 128, True, "none", False, False, {}),
     ("bf16", 2, 8192, 48, 32, True, "none", False, False, {}),
+    # the other shapes of a workgroup: by outputs, rows and inputs
+    ("bf16", 12, 1500, 333, 64, True, "none", True, False, {}),
+    ("f16", 3, 300, 8200, 128, False, "none", True, False, {}),
+    ("bf16", 11, 2090, 8200, 32, True, "relu", False, False, {}),
+    ("f16", 16, 777, 16400, 64, True, "none", False, False, {}),
+    ("bf16", 9, 1160, 32790, 128, True, "none", True, True, {}),
 ]
 
 
