@@ -23,6 +23,13 @@ __device__ __forceinline__ float softplus(float x) {
     return fmaxf(x, 0.0f) + fmaf(__builtin_amdgcn_logf(w), kLn2, lost);
 }
 
+// A log2(e), for exp(d A) = exp2(d (A log2(e))). A finite A stays finite, so that a step of zero
+// keeps the state: one past 2.36e38 counts as that.
+__device__ __forceinline__ float rate_base2(float A) {
+    const float r = A * kLog2e;
+    return __builtin_isinf(r) && !__builtin_isinf(A) ? __builtin_copysignf(__FLT_MAX__, A) : r;
+}
+
 // ---------------------------------------------------------------------------- prompts
 
 // What a launch adds to the arguments: how the work is cut.
@@ -87,7 +94,8 @@ template <int NS> __device__ __forceinline__ void load_states(const float *row, 
 //   2. each wave runs its states over the tile: per state and token one exp2 (two issue
 //      slots), two products and two multiply-adds, and leaves its part of y in LDS;
 //   3. all threads add the NW parts, the skip and the gate, and store y.
-// Past the chunk's end d = d * u = 0, which keeps the states as they are.
+// The last tile stops at the chunk's end: a token of no step would not do there, as 0 * A is NaN
+// for an infinite A.
 // Bound by the vector ALU: 6 N issue slots of four cycles a token and channel, and about 38 for
 // the step size, gate, conversions and sums, against 4 values moved. Measured, bf16, 16
 // states: 16384 ragged tokens x 4096 channels 247 to 261 us, the ALUs 93 % busy; one sequence of
@@ -157,7 +165,7 @@ __global__ __launch_bounds__(64 * NW, NW <= 2 ? 4 : NW <= 8 ? 5 : NS == 4 ? 8 : 
     if (starts) load_states<NS>(state, wave * NS, a.states, k.vec, h);
 #pragma unroll
     for (int i = 0; i < NS; i++) {
-        A[i] *= kLog2e;
+        A[i] = rate_base2(A[i]);
         if (!starts) h[i] = 0.0f;
     }
     if (FIRST && chunk == 0) {
@@ -252,21 +260,20 @@ __global__ __launch_bounds__(64 * NW, NW <= 2 ? 4 : NW <= 8 ? 5 : NS == 4 ? 8 : 
 #pragma unroll
         for (int e = 0; e < EPT; e++) {
             const int tt = e * NW + wave;
-            const bool in = kFull || t0 + tt < end;
-            if (kEven || tt < TT) s_d[tt][lane] = in ? float2{d[e], d[e] * x[e]} : float2{0.0f, 0.0f};
-            if (FIRST && in && (kEven || tt < TT)) dsum += d[e];
+            if (kEven || tt < TT) s_d[tt][lane] = float2{d[e], d[e] * x[e]};
+            if (FIRST && (kEven || tt < TT) && (kFull || t0 + tt < end)) dsum += d[e];
         }
 #pragma unroll
         for (int e = 0; e < BCE; e++) {
             const int i = e * 64 * NW + threadIdx.x;
-            const bool in = i % NP < a.states && (kFull || t0 + i / NP % TT < end);
-            if (!FIRST || i < TT * NP) (&s_bc[0][0][0])[i] = in ? to_f32(nbc[e]) : 0.0f;
+            if (!FIRST || i < TT * NP) (&s_bc[0][0][0])[i] = i % NP < a.states ? to_f32(nbc[e]) : 0.0f;
         }
         fetch(t0 + TT);
         __syncthreads();
         if (wave < waves) {
 #pragma unroll
             for (int t = 0; t < TT; t++) {
+                if (!kFull && t0 + t >= end) break;
                 const float2 v = s_d[t][lane];
                 float sum = 0.0f;
 #pragma unroll
@@ -388,7 +395,7 @@ __global__ __launch_bounds__(kBlock) void scan_token_kernel(const selective_scan
         at[i] = has[i] ? n : 0;
         const Pack<float, VEC> v = load_pack<float, VEC>(a.a + (long long)c * a.states + at[i]);
 #pragma unroll
-        for (int j = 0; j < VEC; j++) A[i][j] = v.v[j] * kLog2e;
+        for (int j = 0; j < VEC; j++) A[i][j] = rate_base2(v.v[j]);
     }
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.0f, skip = a.skip ? a.skip[c] : 0.0f;
 

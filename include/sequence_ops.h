@@ -70,7 +70,10 @@ int causal_conv1d_step(const causal_conv1d_args *args, void *stream);
  *     h[c, n] = exp(d * a[c, n]) * h[c, n] + d * u[t, c] * b[t, g, n]
  *     y[t, c] = sum_n h[c, n] * c[t, g, n] + skip[c] * u[t, c]
  *     y[t, c] *= gate[t, c] / (1 + exp(-gate[t, c]))     (with a gate)
- * The state and every intermediate are fp32; y is rounded once. */
+ * The state and every intermediate are fp32; y is rounded once. A finite a counts as at most
+ * 2.36e38 in magnitude; where one is -infinity, a state forgets at every step that is not zero.
+ * An infinity or NaN in an input may make y, and through the state the later y, infinite or NaN
+ * in the channels and the sequence that read it, and in no others. */
 typedef struct selective_scan_args {
     const void *u, *dt;    /* token rows of `channels` values */
     const float *a;        /* [channels, states], contiguous */

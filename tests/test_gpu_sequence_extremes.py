@@ -1,0 +1,78 @@
+"""Causal convolution, selective scan and 4-bit products with values at the ends of their types, against their
+definitions in 64 bits."""
+import pytest
+import torch
+
+import sequence_reference as ref
+from test_gpu_sequence import DEV, _normal, _on, _reference, _rng, _scan_args, _scan_case
+
+pytestmark = pytest.mark.gpu
+
+c2d = pytest.importorskip("conv2d_bias_activation_amd")
+
+
+# type, lengths, packed, channels, states, groups: every number of states that has a kernel of its own, ends inside a
+# tile, sequences that are split and that are not
+FAST = [("f32", [37], False, 64, 16, 1), ("bf16", [33, 0, 1, 2, 70, 17], True, 72, 16, 1), ("f16", [13], False, 40, 3, 1),
+        ("f32", [21, 9], True, 36, 6, 2), ("f32", [29], False, 20, 32, 1), ("bf16", [19], False, 24, 50, 1),
+        ("f32", [15, 3], True, 16, 100, 1), ("f32", [11], False, 8, 200, 1), ("f32", [901], False, 64, 16, 1),
+        ("bf16", [1001, 5, 700], True, 40, 8, 1), ("f32", [603], False, 24, 64, 2)]
+
+
+@pytest.mark.parametrize("kind,lengths,packed,d,n,groups", FAST)
+@pytest.mark.parametrize("rate", [-float("inf"), -3e38])
+def test_rates_without_bounds(rate, kind, lengths, packed, d, n, groups):
+    """A state whose rate A is infinite, or so large that A log2(e) is, forgets at once: exp(d A) is zero for every
+    step of these sequences, so the definition's values are those of A = -1e30."""
+    c = _scan_case(61, kind, lengths, d, n, groups, {})
+    c["A"] = c["A"].clone()
+    c["A"][:, ::3] = -1e30
+    want, bound, state, state_bound = _reference(c, lengths)
+    c["A"][:, ::3] = rate
+    _, args, kw = _scan_args(c, lengths, packed, {})
+    for workspace in (None, False):
+        dev_state = _on(c["state"])
+        y = c2d.selective_scan(*args, **kw, state=dev_state, longest=max(lengths), workspace=workspace)
+        ref.close(y.reshape(-1, d), want, bound, "y")
+        ref.close(dev_state, state, state_bound, "state")
+
+
+@pytest.mark.parametrize("n", [4, 5, 16, 64, 130])
+def test_token_rates_without_bounds(n):
+    c = _scan_case(62, "f32", [1] * 3, 48, n, 1, {})
+    c["A"] = c["A"].clone()
+    c["A"][:, ::2] = -1e30
+    want, bound, state, state_bound = _reference(c, [1] * 3)
+    for rate in (-float("inf"), -3e38):
+        c["A"][:, ::2] = rate
+        _, args, kw = _scan_args(c, [1] * 3, True, {})
+        del kw["seq_offsets"]
+        dev_state = _on(c["state"])
+        ref.close(c2d.selective_scan_step(*args, **kw, state=dev_state), want, bound, "y")
+        ref.close(dev_state, state, state_bound, "state")
+
+
+@pytest.mark.parametrize("lengths,n", [([45], 16), ([700], 16), ([21], 5)])
+def test_empty_steps_keep_the_largest_finite_rates(lengths, n):
+    """exp(0 A) = 1 for any finite A: a token without a step leaves the state as it is."""
+    c = _scan_case(63, "f32", lengths, 64, n, 1, {"plain": True})
+    c["A"] = c["A"].clone()
+    c["A"][:, ::2] = -3.4e38
+    c["dt"][2:] = 0.0
+    want, bound, state, state_bound = _reference(c, lengths)
+    _, args, kw = _scan_args(c, lengths, False, {})
+    for workspace in (None, False):
+        dev_state = _on(c["state"])
+        y = c2d.selective_scan(*args, **kw, state=dev_state, workspace=workspace)
+        ref.close(y.reshape(-1, 64), want, bound, "y")
+        ref.close(dev_state, state, state_bound, "state")
+    c = _scan_case(64, "f32", [1] * 2, 64, n, 1, {"plain": True})
+    c["A"] = c["A"].clone()
+    c["A"][:, 1::2] = -3.4e38
+    c["dt"][:] = 0.0
+    want, bound, state, state_bound = _reference(c, [1] * 2)
+    _, args, kw = _scan_args(c, [1] * 2, True, {})
+    del kw["seq_offsets"]
+    dev_state = _on(c["state"])
+    ref.close(c2d.selective_scan_step(*args, **kw, state=dev_state), want, bound, "y")
+    ref.close(dev_state, state, state_bound, "state")
