@@ -11,15 +11,17 @@ raises.
 Workspace: the library allocates no device memory; kernel variants that need
 scratch use a caller-owned workspace registered per thread and device. Every call
 here takes ``workspace=``: ``None`` (default) uses a buffer this module keeps per
-(device, stream), allocated with torch.empty and grown to what the call's preferred
-variant needs (so calls on different streams never share one); ``False`` runs the
+(device, stream, host thread), allocated with torch.empty and grown to what the call's
+preferred variant needs (so calls on different streams never share one, nor do calls of
+two threads on one stream, whose kernels may be enqueued in turn); ``False`` runs the
 call without a workspace (variants that need none); a uint8 CUDA tensor is used as
-given.
+given, and two threads must not give the same one at the same time.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 import torch
 
@@ -173,7 +175,8 @@ def _ptr(t):
 
 
 DEFAULT_WORKSPACE_BYTES = 64 << 20
-_ws_cache = {}  # (device index, stream handle) -> uint8 tensor
+_ws_cache = {}  # _ws_key -> uint8 tensor
+_main_thread = threading.main_thread().ident
 
 
 def set_workspace(ws, device=None):
@@ -195,8 +198,16 @@ def _stream_of(device, stream):
     return torch.cuda.current_stream(device) if stream is None else stream
 
 
+def _ws_key(index, handle):
+    """Key of the default workspace on a device and stream: (device index, stream handle) in the
+    main thread, with the thread's number behind them in others. A number that a later thread has
+    again gives it a buffer whose users are queued before it on its stream."""
+    thread = threading.get_ident()
+    return (index, handle) if thread == _main_thread else (index, handle, thread)
+
+
 def _default_workspace(device, stream, need):
-    key = (device.index if device.index is not None else torch.cuda.current_device(), stream.cuda_stream)
+    key = _ws_key(device.index if device.index is not None else torch.cuda.current_device(), stream.cuda_stream)
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < need:
         # torch's allocator is stream-ordered: the old buffer is reused only by work

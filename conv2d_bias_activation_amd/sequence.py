@@ -18,7 +18,7 @@ import struct
 
 import torch
 
-from . import _ACTS, _DTYPES, RES_BEFORE_ACT, _check, _load, _use_workspace, _ws_cache
+from . import _ACTS, _DTYPES, RES_BEFORE_ACT, _check, _load, _use_workspace, _ws_cache, _ws_key
 
 __all__ = ["causal_conv1d", "causal_conv1d_step", "selective_scan", "selective_scan_step", "w4_pack", "matvec_w4",
            "W4Weights"]
@@ -66,7 +66,7 @@ def _scratch(device, stream, workspace, need):
     """Registers the workspace of a call. The default one is allocated on the call's stream, so
     that one that has to grow is freed behind the work that still uses it."""
     if workspace is None and device.index == _current_device():
-        ws = _ws_cache.get((device.index, _raw_stream(device.index) if stream is None else stream.cuda_stream))
+        ws = _ws_cache.get(_ws_key(device.index, _raw_stream(device.index) if stream is None else stream.cuda_stream))
         if ws is not None and ws.numel() >= need:  # as below, without the detours
             _check(_load().conv2d_set_workspace(ws.data_ptr(), ws.numel()))
             return

@@ -38,7 +38,9 @@
  *    conv2d_workspace_size and conv2d_stack_workspace_size report how much the
  *    preferred variants use. Two calls that may run at the same time (on two streams)
  *    must not share a workspace; a call reads and writes its workspace only on its own
- *    stream, in its own launches, so calls queued on one stream may share one.
+ *    stream, in its own launches, so calls that one thread queues on one stream may share
+ *    one. A call may be several launches: two threads that queue calls on one stream at the
+ *    same time need a workspace each.
  *  - Other state kept between calls: the last-error message (per thread), the
  *    compute-unit count and arch name of each device (queried once), the registered
  *    workspaces (per thread and device) and the tuned-plan table (conv2d_tune).
