@@ -210,9 +210,10 @@ def _default_workspace(device, stream, need):
     key = _ws_key(device.index if device.index is not None else torch.cuda.current_device(), stream.cuda_stream)
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < need:
-        # torch's allocator is stream-ordered: the old buffer is reused only by work
-        # queued after the calls that still use it on this stream
-        ws = torch.empty(max(need, DEFAULT_WORKSPACE_BYTES), dtype=torch.uint8, device=device)
+        # torch's allocator is stream-ordered: allocated on the call's stream, the old buffer
+        # is reused only by work queued after the calls that still use it there
+        with torch.cuda.stream(stream):
+            ws = torch.empty(max(need, DEFAULT_WORKSPACE_BYTES), dtype=torch.uint8, device=device)
         _ws_cache[key] = ws
     return ws
 

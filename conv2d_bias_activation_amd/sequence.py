@@ -63,16 +63,13 @@ def _new_like(x, stream):
 
 
 def _scratch(device, stream, workspace, need):
-    """Registers the workspace of a call. The default one is allocated on the call's stream, so
-    that one that has to grow is freed behind the work that still uses it."""
+    """Registers the workspace of a call."""
     if workspace is None and device.index == _current_device():
         ws = _ws_cache.get(_ws_key(device.index, _raw_stream(device.index) if stream is None else stream.cuda_stream))
         if ws is not None and ws.numel() >= need:  # as below, without the detours
             _check(_load().conv2d_set_workspace(ws.data_ptr(), ws.numel()))
             return
-    st = torch.cuda.current_stream(device) if stream is None else stream
-    with torch.cuda.stream(st):
-        _use_workspace(device, st, workspace, need)
+    _use_workspace(device, torch.cuda.current_stream(device) if stream is None else stream, workspace, need)
 
 
 def _fail(name, what):

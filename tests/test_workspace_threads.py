@@ -80,3 +80,17 @@ def test_scans_from_two_threads_on_one_stream():
         assert len(got[i]) == 100
         for y in got[i]:
             assert torch.equal(y, want[i])
+
+
+@pytest.mark.gpu
+def test_default_workspace_belongs_to_the_calls_stream():
+    """A buffer that is dropped when a larger one takes its place may only be reused behind the calls that still work
+    in it: it has to be allocated on their stream, whichever is current."""
+    side = torch.cuda.Stream()
+    x = torch.randn(2, 20, 20, 512, device="cuda").bfloat16()
+    w = torch.randn(128, 3, 3, 512, device="cuda").bfloat16()
+    c2d.conv2d_fused(x, w, pad=1, stream=side)
+    ws = c2d._ws_cache[(torch.cuda.current_device(), side.cuda_stream)]
+    torch.cuda.synchronize()
+    here = [s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] <= ws.data_ptr() < s["address"] + s["total_size"]]
+    assert here == [side.cuda_stream]
