@@ -52,10 +52,14 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(const uint8_t *codes, cons
 template <typename T> struct Frag;
 template <> struct Frag<bf16> {
     typedef bf16 v8 __attribute__((ext_vector_type(8)));
-    static constexpr uint32_t kOnes = 0x3f803f80u;
-    // 16 + q for the codes of pair p: q in the upper four mantissa bits of 16.0
+    // Everything that meets x is 2^-12 of its value, so that the sums of a group, with its offset
+    // of up to 31 a code, stay in range for any finite x; the products of even the smallest x
+    // are still exact in fp32, as multiples of 2^-145.
+    static constexpr float kUnit = 4096.0f;
+    static constexpr uint32_t kOnes = 0x39803980u;
+    // 16 + q for the codes of pair p: q in the upper four mantissa bits of 16
     static __device__ __forceinline__ uint32_t pair(uint32_t w, int p) {
-        return ((p == 0 ? w << 3 : w >> (4 * p - 3)) & 0x00780078u) | 0x41804180u;
+        return ((p == 0 ? w << 3 : w >> (4 * p - 3)) & 0x00780078u) | 0x3b803b80u;
     }
     static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
@@ -63,6 +67,7 @@ template <> struct Frag<bf16> {
 };
 template <> struct Frag<f16> {
     typedef f16 v8 __attribute__((ext_vector_type(8)));
+    static constexpr float kUnit = 1.0f;
     static constexpr uint32_t kOnes = 0x3c003c00u;
     static __device__ __forceinline__ uint32_t pair(uint32_t w, int p) {
         return ((p < 2 ? w << (6 - 4 * p) : w >> (4 * p - 6)) & 0x03c003c0u) | 0x4c004c00u;
@@ -113,8 +118,9 @@ template <int NT, int MT, int PER> struct Block {
 // The matrix cores take x as the A operand and the codes, as the exact 16-bit values 16 + q, as
 // B: two instructions for two codes, and no multiplication with scales before the sum. With S
 // the sum of the same inputs (x times ones), a group's part of an output is
-// scale * (sum of x (16 + q) - (16 + zero) S), in fp32; the offset costs a factor of about
-// five in the sums' rounding error, which stays under 1e-6 of the output. Bound by the bytes
+// scale * (sum of x (16 + q) - (16 + zero) S), in fp32. Its rounding error is a few 2^-24 of
+// scale * (sum of |x|) * (47 + zero), five times what the codes without the offset would have
+// (little beside y's own rounding but where a row's products cancel). Bound by the bytes
 // of the packed weights where there are many (16 rows, 8192 -> 32768: 38 us, 3.9 TB/s), else by
 // the latency of a wave's few blocks (1 row, 2048 -> 4096: 3.8 us of kernel).
 template <typename T, int NT, int MT, int W, int PER, bool ZEROS>
@@ -218,7 +224,7 @@ __global__ __launch_bounds__(64 * W) void matvec_w4_kernel(const matvec_w4_args 
 #pragma unroll
         for (int w = 0; w < W; w++) sum += s_sum[w][t][l][r];
         const float res = a.residual ? to_f32(static_cast<const T *>(a.residual)[m * a.residual_row + n]) : 0.0f;
-        const float v = epilogue(sum, a.bias ? a.bias[n] : 0.0f, act == CONV2D_ACT_PRELU ? a.alpha[n] : 0.0f, res,
+        const float v = epilogue(sum * Frag<T>::kUnit, a.bias ? a.bias[n] : 0.0f, act == CONV2D_ACT_PRELU ? a.alpha[n] : 0.0f, res,
                                  a.residual != nullptr, act, (a.act & CONV2D_RES_BEFORE_ACT) != 0);
         static_cast<T *>(a.y)[m * a.y_row + n] = round_fp32<T>(v);
     }

@@ -76,3 +76,26 @@ def test_empty_steps_keep_the_largest_finite_rates(lengths, n):
     dev_state = _on(c["state"])
     ref.close(c2d.selective_scan_step(*args, **kw, state=dev_state), want, bound, "y")
     ref.close(dev_state, state, state_bound, "state")
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("size", [1e-37, 1e-30, 2e38])
+@pytest.mark.parametrize("rows,k,n,group", [(1, 256, 64, 128), (5, 401, 130, 32), (17, 640, 48, 64)])
+def test_products_of_the_largest_and_smallest_rows(rows, k, n, group, size, zeros):
+    """bf16 reaches from 1e-38 to 3e38. Rows of values near either end give finite products and, as the scales bring
+    them back to moderate numbers, the definition's."""
+    g = _rng(66)
+    x = (torch.rand(rows, k, generator=g) * 0.5 + 0.5) * size * torch.sign(torch.randn(rows, k, generator=g))
+    if size > 1:  # sums of the products themselves stay in range: one large value for each group
+        x = torch.where(torch.arange(k) % group == 3, x / 15, x * 2.0 ** -40)
+    x = x.bfloat16()
+    groups = -(-k // group)
+    codes = torch.randint(0, 256, (n, (k + 1) // 2), generator=g, dtype=torch.uint8)
+    scales = ((torch.rand(n, groups, generator=g) + 0.5) / size).bfloat16()
+    z = torch.randint(0, 16, (n, groups), generator=g, dtype=torch.uint8) if zeros else None
+    want, bound = ref.w4(x, codes, scales, z, group, None, None, None, "none", False)
+    # a product below fp32's smallest normal number may be off by half of its smallest step, 2^-150, times the scale, or by
+    # 2^12 as much where codes are taken times 2^-12
+    bound = bound + k * 2.0 ** -138 * scales.double().max()
+    weights = c2d.w4_pack(_on(codes), _on(scales), _on(z), in_features=k, group=group)
+    ref.close(c2d.matvec_w4(_on(x), weights), want, bound, "w4")
