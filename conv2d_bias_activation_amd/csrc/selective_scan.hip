@@ -42,7 +42,7 @@ struct ScanCut {
     float *ws;    // split sequences: a record per item, see Record
 };
 
-// Record of a chunk of a split sequence, left by the first pass for the second: the sum of
+// Record of a chunk of a split sequence, left by the first pass for the second: half the sum of
 // its step sizes [channels], then its end state [states][channels], from a zero start state
 // (the first chunk: from the sequence's own). The last chunk's end state is of no use to
 // another chunk; its place takes the sequence's start state, which the second pass could
@@ -237,7 +237,12 @@ __global__ __launch_bounds__(64 * NW, NW <= 2 ? 4 : NW <= 8 ? 5 : NS == 4 ? 8 : 
             for (int m = 0; m < kAhead; m++)
                 if (j + m < chunk) {
 #pragma unroll
-                    for (int i = 0; i < NS; i++) h[i] = fmaf(__builtin_amdgcn_exp2f(sum[m] * A[i]), h[i], add[m][i]);
+                    for (int i = 0; i < NS; i++) {
+                        // A chunk's decay in two equal factors: rates or steps of the other sign may
+                        // make it pass fp32's range while the state, zero or tiny, does not.
+                        const float e = __builtin_amdgcn_exp2f(fminf(sum[m] * A[i], 127.0f));
+                        h[i] = fmaf(e, e * h[i], add[m][i]);
+                    }
                 }
         }
 #pragma unroll
@@ -322,7 +327,7 @@ __global__ __launch_bounds__(64 * NW, NW <= 2 ? 4 : NW <= 8 ? 5 : NS == 4 ? 8 : 
     if (!on || wave >= waves) return;
     if (FIRST) {
         float *p = record(a, k, item) + c;
-        if (wave == 0) p[0] = dsum;
+        if (wave == 0) p[0] = 0.5f * dsum;
 #pragma unroll
         for (int i = 0; i < NS; i++)
             if (wave * NS + i < a.states) p[(long long)(wave * NS + i + 1) * a.channels] = h[i];

@@ -99,3 +99,26 @@ def test_products_of_the_largest_and_smallest_rows(rows, k, n, group, size, zero
     bound = bound + k * 2.0 ** -138 * scales.double().max()
     weights = c2d.w4_pack(_on(codes), _on(scales), _on(z), in_features=k, group=group)
     ref.close(c2d.matvec_w4(_on(x), weights), want, bound, "w4")
+
+
+@pytest.mark.parametrize("d", [40, 64])
+def test_growth_past_a_chunk(d):
+    """Steps may be negative or rates positive. A state that is zero stays so however far the decay of a whole chunk
+    passes fp32's range, and one that grows and shrinks again by e^96 keeps its value."""
+    tokens, n = 900, 16
+    c = _scan_case(65, "f32", [tokens], d, n, 1, {"plain": True})
+    c["A"] = torch.ones(d, n)
+    place = torch.arange(tokens)
+    c["dt"] = torch.where(place // 32 % 2 == 0, 3.0, -3.0)[:, None].repeat(1, d)  # a sum of 96 in 32 tokens
+    c["dt"][896:] = 0.125
+    c["u"][:896] = 0.0
+    c["state"] = torch.full((1, d, n), 1e-36)
+    c["state"][:, ::2] = 0.0
+    want, bound, state, state_bound = _reference(c, [tokens])
+    assert all(torch.isfinite(t).all() for t in (want, bound, state, state_bound))
+    _, args, kw = _scan_args(c, [tokens], False, {})
+    for workspace in (False, None):
+        dev_state = _on(c["state"])
+        y = c2d.selective_scan(*args, **kw, state=dev_state, workspace=workspace)
+        ref.close(y.reshape(-1, d), want, bound, "y")
+        ref.close(dev_state, state, state_bound, "state")
