@@ -183,16 +183,15 @@ template <typename T, int VEC, int W, int kRun> hipError_t launch_prompt(const c
     const int runs = (int)((a.tokens + kRun - 1) / kRun);
     const long long items = a.offsets ? a.tokens / kRun + a.nseq : (long long)(runs ? runs : 1) * a.nseq;
     const long long blocks = (items + kBlock / tx - 1) / (kBlock / tx) * cblocks;
-    return launch_kernel(causal_conv_kernel<T, VEC, W, kRun>, dim3((unsigned)blocks), dim3(kBlock), 0, st, a, tx, cblocks,
-                         (int)items, runs ? runs : 1);
+    return launch_blocks(causal_conv_kernel<T, VEC, W, kRun>, blocks, kBlock, st, a, tx, cblocks, (int)items,
+                         runs ? runs : 1);
 }
 
 template <typename T, int VEC, int W> hipError_t launch_w(const causal_conv1d_args &a, bool step, hipStream_t st) {
     const int nvec = (a.channels + VEC - 1) / VEC;
     if (step) {
         const int cblocks = (nvec + kBlock - 1) / kBlock;
-        return launch_kernel(causal_conv_step_kernel<T, VEC, W>, dim3((unsigned)((long long)cblocks * a.nseq)),
-                             dim3(kBlock), 0, st, a, cblocks);
+        return launch_blocks(causal_conv_step_kernel<T, VEC, W>, (long long)cblocks * a.nseq, kBlock, st, a, cblocks);
     }
     // Short runs make many threads and a short walk for each; long ones read fewer rows twice
     // and load the weights less often. Times in us of runs of 4, 16 and 32 (bf16, width 4):

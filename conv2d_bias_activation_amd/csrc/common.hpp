@@ -19,6 +19,15 @@ inline hipError_t launch_kernel(void (*k)(P...), dim3 grid, dim3 block, size_t s
     return hipLaunchKernel(reinterpret_cast<const void *>(k), grid, block, ptrs, smem, st);
 }
 
+// launch_kernel for a one-dimensional grid whose size comes from the call's arguments. A launch
+// holds fewer than 2^32 threads; for more, hipErrorInvalidConfiguration and nothing launched.
+template <typename... P>
+inline hipError_t launch_blocks(void (*k)(P...), long long blocks, int threads, hipStream_t st,
+                                std::type_identity_t<P>... args) {
+    if (blocks > 0xffffffffll / threads) return hipErrorInvalidConfiguration;
+    return launch_kernel(k, dim3((unsigned)blocks), dim3(threads), 0, st, args...);
+}
+
 typedef __bf16 bf16;
 typedef _Float16 f16;
 typedef float f32x4 __attribute__((ext_vector_type(4)));

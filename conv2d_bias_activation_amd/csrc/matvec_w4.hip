@@ -239,7 +239,7 @@ template <typename T, int NT, int MT, int W, int PER, bool ZEROS> hipError_t lau
     const uint8_t *zeros = reinterpret_cast<const uint8_t *>(scales + nt * kTileN * PER);
     const int nblocks = ((a.out_features + kTileN - 1) / kTileN + NT - 1) / NT;
     const long long mblocks = (a.rows + 16 * MT - 1) / (16 * MT);
-    return launch_kernel(matvec_w4_kernel<T, NT, MT, W, PER, ZEROS>, dim3((unsigned)(nblocks * mblocks)), dim3(64 * W), 0, st, a,
+    return launch_blocks(matvec_w4_kernel<T, NT, MT, W, PER, ZEROS>, nblocks * mblocks, 64 * W, st, a,
                          static_cast<const u32x4 *>(a.packed), scales, zeros, nblocks);
 }
 

@@ -346,12 +346,12 @@ __global__ __launch_bounds__(64 * NW, NW <= 2 ? 4 : NW <= 8 ? 5 : NS == 4 ? 8 : 
 }
 
 template <typename T, int NS, int NW> hipError_t launch_prompt(const selective_scan_args &a, const ScanCut &k, hipStream_t st) {
-    const dim3 grid((unsigned)((long long)k.items * k.cblocks * a.groups)), block(64 * NW);
+    const long long blocks = (long long)k.items * k.cblocks * a.groups;
     if (k.ws) {
-        const hipError_t e = launch_kernel(scan_prompt_kernel<T, NS, NW, true>, grid, block, 0, st, a, k);
+        const hipError_t e = launch_blocks(scan_prompt_kernel<T, NS, NW, true>, blocks, 64 * NW, st, a, k);
         if (e != hipSuccess) return e;
     }
-    return launch_kernel(scan_prompt_kernel<T, NS, NW, false>, grid, block, 0, st, a, k);
+    return launch_blocks(scan_prompt_kernel<T, NS, NW, false>, blocks, 64 * NW, st, a, k);
 }
 
 template <typename T> hipError_t launch_prompt_t(const selective_scan_args &a, const ScanCut &k, hipStream_t st) {
@@ -456,9 +456,8 @@ template <typename T, int VEC, int S> hipError_t launch_token(const selective_sc
     // two sequences a workgroup where that leaves the card full (512 sequences x 4096 channels x
     // 16 states: 59.4 us, 4.8 TB/s; one: 63.1, four: 59.9, eight: 71.0), else one
     if (S == 1 && blocks >= 4096)
-        return launch_kernel(scan_token_kernel<T, VEC, S, 2>, dim3((unsigned)(cblocks * ((a.nseq + 1ll) / 2))),
-                             dim3(kBlock), 0, st, a, lanes, cblocks);
-    return launch_kernel(scan_token_kernel<T, VEC, S, 1>, dim3((unsigned)blocks), dim3(kBlock), 0, st, a, lanes, cblocks);
+        return launch_blocks(scan_token_kernel<T, VEC, S, 2>, cblocks * ((a.nseq + 1ll) / 2), kBlock, st, a, lanes, cblocks);
+    return launch_blocks(scan_token_kernel<T, VEC, S, 1>, blocks, kBlock, st, a, lanes, cblocks);
 }
 
 template <typename T> hipError_t launch_token_t(const selective_scan_args &a, hipStream_t st) {

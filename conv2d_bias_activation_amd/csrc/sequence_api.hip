@@ -10,7 +10,6 @@ namespace {
 using namespace c2d;
 
 constexpr long long kMaxTokens = 1ll << 30;
-constexpr long long kMaxBlocks = 1ll << 31;  // workgroups of a launch
 
 // Memory that a call reads or writes.
 struct Extent {
@@ -102,8 +101,11 @@ int check_act(const char *op, int act, const float *alpha, int flags) {
     return CONV2D_OK;
 }
 
-int too_many_blocks(const char *op) {
-    return set_error(CONV2D_EUNSUPPORTED, "%s: too many channels and sequences for one launch", op);
+// The status of a call whose kernels were launched with `e`.
+int launched(const char *op, hipError_t e) {
+    if (e == hipErrorInvalidConfiguration)  // from launch_blocks
+        return set_error(CONV2D_EUNSUPPORTED, "%s: 2^32 threads or more, too many for one launch", op);
+    return e == hipSuccess ? set_ok() : hip_fail(e, op);
 }
 
 int run_conv(const causal_conv1d_args *args, bool step, void *stream) {
@@ -139,11 +141,7 @@ int run_conv(const causal_conv1d_args *args, bool step, void *stream) {
     const bool vec = a.channels % V == 0 && aligned16(a.x) && aligned16(a.y) && aligned16(a.w) && aligned16(a.state) &&
                      a.x_token % V == 0 && a.y_token % V == 0 &&
                      (s.packed || step || (a.x_batch % V == 0 && a.y_batch % V == 0));
-    // an upper bound of the workgroups of either kernel
-    if ((s.rows() / 4 + 2ll * s.nseq + 1) * (a.channels / (vec ? V : 1) / 64 + 1) >= kMaxBlocks)
-        return too_many_blocks(op);
-    const hipError_t e = launch_causal_conv(a, vec, step, static_cast<hipStream_t>(stream));
-    return e == hipSuccess ? set_ok() : hip_fail(e, op);
+    return launched(op, launch_causal_conv(a, vec, step, static_cast<hipStream_t>(stream)));
 }
 
 // Validates a scan's arguments.
@@ -183,11 +181,7 @@ int check_scan(const selective_scan_args *args, const char *op, bool step) {
     const Extent eo{"offsets", a.offsets, 4ll * (a.nseq + 1ll)}, el{"slots", a.slots, 4ll * a.nseq};
     rc = check_no_overlap(op, ey, {in[0], in[1], in[2], in[3], in[5], es, ea, ek, eb, eo, el});
     if (!rc) rc = check_no_overlap(op, es, {in[0], in[1], in[2], in[3], in[5], ea, ek, eb, eo, el});
-    if (rc) return rc;
-    // an upper bound of the workgroups of either kernel (a split prompt adds at most 5120 chunks)
-    if (((long long)a.channels * (step ? a.states : 4) / 256 + a.groups + 1) * (2ll * s.nseq + 5120) >= kMaxBlocks)
-        return too_many_blocks(op);
-    return CONV2D_OK;
+    return rc;
 }
 
 int run_scan(const selective_scan_args *args, bool step, void *stream) {
@@ -197,8 +191,7 @@ int run_scan(const selective_scan_args *args, bool step, void *stream) {
     if (args->nseq == 0) return set_ok();
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const Workspace ws = step ? Workspace{} : current_ws();
-    const hipError_t e = step ? launch_scan_token(*args, st) : launch_scan(*args, ws.p, ws.bytes, st);
-    return e == hipSuccess ? set_ok() : hip_fail(e, op);
+    return launched(op, step ? launch_scan_token(*args, st) : launch_scan(*args, ws.p, ws.bytes, st));
 }
 
 int check_w4(const char *op, int out_features, int in_features, int group) {
@@ -287,10 +280,7 @@ int matvec_w4(const matvec_w4_args *args, void *stream) {
                            Extent{"bias", a.bias, 4ll * a.out_features},
                            Extent{"alpha", (a.act & 0xff) == CONV2D_ACT_PRELU ? a.alpha : nullptr, 4ll * a.out_features}});
     if (rc) return rc;
-    if ((a.out_features / 16 + 1ll) * a.rows >= kMaxBlocks)
-        return set_error(CONV2D_EUNSUPPORTED, "%s: too many rows for one launch", op);
-    const hipError_t e = launch_matvec_w4(a, static_cast<hipStream_t>(stream));
-    return e == hipSuccess ? set_ok() : hip_fail(e, op);
+    return launched(op, launch_matvec_w4(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
