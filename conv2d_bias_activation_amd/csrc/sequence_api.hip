@@ -10,6 +10,9 @@ namespace {
 using namespace c2d;
 
 constexpr long long kMaxTokens = 1ll << 30;
+// Channels of a token, and inputs or outputs of a product: the kernels round them up to whole
+// blocks and tiles in 32 bits.
+constexpr int kMaxWidth = 1 << 30;
 
 // Memory that a call reads or writes.
 struct Extent {
@@ -101,6 +104,10 @@ int check_act(const char *op, int act, const float *alpha, int flags) {
     return CONV2D_OK;
 }
 
+int too_wide(const char *op) {
+    return set_error(CONV2D_EUNSUPPORTED, "%s: more than 2^30 channels, inputs or outputs are not supported", op);
+}
+
 // The status of a call whose kernels were launched with `e`.
 int launched(const char *op, hipError_t e) {
     if (e == hipErrorInvalidConfiguration)  // from launch_blocks
@@ -116,6 +123,7 @@ int run_conv(const causal_conv1d_args *args, bool step, void *stream) {
     int rc = check_shape(&s, a.offsets, a.slots, a.state_rows);
     if (rc) return rc;
     if (a.channels <= 0) return set_error(CONV2D_EINVAL, "%s: channels must be positive (got %d)", op, a.channels);
+    if (a.channels > kMaxWidth) return too_wide(op);
     if (a.width < 2 || a.width > 4) return set_error(CONV2D_EINVAL, "%s: width must be 2, 3 or 4 (got %d)", op, a.width);
     rc = check_act(op, a.act, a.alpha, 0);
     if (rc) return rc;
@@ -154,6 +162,7 @@ int check_scan(const selective_scan_args *args, const char *op, bool step) {
     if (a.channels <= 0 || a.groups <= 0 || a.channels % a.groups)
         return set_error(CONV2D_EINVAL, "%s: channels must be a positive multiple of groups (got %d and %d)", op,
                          a.channels, a.groups);
+    if (a.channels > kMaxWidth) return too_wide(op);
     if (a.states < 1 || a.states > 256)
         return set_error(CONV2D_EINVAL, "%s: states must be 1 to 256 (got %d)", op, a.states);
     if (a.longest < 0) return set_error(CONV2D_EINVAL, "%s: longest must not be negative", op);
@@ -199,8 +208,9 @@ int check_w4(const char *op, int out_features, int in_features, int group) {
         return set_error(CONV2D_EINVAL, "%s: sizes must be positive (out %d, in %d)", op, out_features, in_features);
     if (group != 32 && group != 64 && group != 128)
         return set_error(CONV2D_EINVAL, "%s: group must be 32, 64 or 128 (got %d)", op, group);
+    if (out_features > kMaxWidth || in_features > kMaxWidth) return too_wide(op);
     if ((long long)out_features * in_features > 1ll << 40)
-        return set_error(CONV2D_EUNSUPPORTED, "%s: 2^40 weights or more are not supported", op);
+        return set_error(CONV2D_EUNSUPPORTED, "%s: more than 2^40 weights are not supported", op);
     return CONV2D_OK;
 }
 

@@ -11,7 +11,8 @@
  *  - Activations are channel-last: the channels of one token are contiguous. Where a struct
  *    has strides (in elements), one token's row and one batch entry's first row may stand
  *    anywhere, so a slice of a wider projection is read in place. Strides may not be negative.
- *  - Offsets into memory are 64-bit; a call may cover up to 2^30 tokens, and where it would
+ *  - Offsets into memory are 64-bit; a call may cover up to 2^30 tokens of up to 2^30 channels
+ *    (inputs and outputs of a product, whose weights may number 2^40), and where it would
  *    need 2^32 GPU threads or more (many short sequences of many channels) it returns
  *    CONV2D_EUNSUPPORTED and has to be made in parts.
  *

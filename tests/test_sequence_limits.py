@@ -1,6 +1,8 @@
 """The largest calls of the sequence operators: what is one too many for a launch is refused by name, what just fits
 gets as far as the device (CPU only)."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -60,3 +62,27 @@ def test_too_many_tokens_are_unsupported():
                  lambda: _many(_scan, step=True, nseq=more), lambda: _many(_w4, rows=more)):
         assert call() == c2d.EUNSUPPORTED
         assert "more than 2^30 tokens" in c2d.last_error()
+
+
+@pytest.mark.parametrize("n", [(1 << 30) + 1, (1 << 31) - 128, (1 << 31) - 1])
+def test_too_wide_is_unsupported(n):
+    """Sizes that 32-bit sums with a tile would overflow."""
+    size = ctypes.c_size_t(0)
+    lib = c2d._load()
+    for call in (lambda: _many(_conv, channels=n), lambda: _many(_conv, step=True, channels=n), lambda: _many(_scan, channels=n),
+                 lambda: _many(_scan, step=True, channels=n), lambda: _many(_w4, in_features=n, out_features=16),
+                 lambda: _many(_w4, in_features=32, out_features=n),
+                 lambda: lib.matvec_w4_packed_bytes(16, n, 128, 0, ctypes.byref(size)),
+                 lambda: lib.matvec_w4_packed_bytes(n, 16, 128, 0, ctypes.byref(size)),
+                 lambda: lib.matvec_w4_pack(FAR, 2 * FAR, None, 3 * FAR, n, 16, 128, c2d.DTYPE_BF16, None)):
+        assert call() == c2d.EUNSUPPORTED
+        assert "more than 2^30 channels, inputs or outputs" in c2d.last_error()
+
+
+def test_packed_size_of_the_widest_weights():
+    size = ctypes.c_size_t(0)
+    packed = c2d._load().matvec_w4_packed_bytes
+    assert packed(16, 1 << 30, 128, 0, ctypes.byref(size)) == c2d.OK and size.value == (1 << 23) * (1024 + 32)
+    assert packed(1 << 30, 127, 128, 1, ctypes.byref(size)) == c2d.OK and size.value == (1 << 26) * (1024 + 48)
+    assert packed((1 << 30) - 1, 1 << 10, 32, 0, ctypes.byref(size)) == c2d.OK and size.value == (1 << 29) * (1024 + 128)
+    assert packed((1 << 30) - 1, (1 << 10) + 1, 32, 0, ctypes.byref(size)) == c2d.EUNSUPPORTED
