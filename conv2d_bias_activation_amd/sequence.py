@@ -29,10 +29,14 @@ _SCAN = struct.Struct("@12P14q8i0q")
 _W4 = struct.Struct("@6P3q7i0q")
 
 
+def _stream_handle(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
 # the current stream's handle and the current device, without what torch.cuda puts around them
-# (a tensor on the GPU has initialised it)
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# (a tensor on the GPU has initialised it); a torch without the private names takes the public way
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_handle)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(name, args, device, stream):
