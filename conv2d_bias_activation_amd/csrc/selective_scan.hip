@@ -39,6 +39,7 @@ struct ScanCut {
     int chunks;   // unpacked: chunks of a sequence
     int cblocks;  // 64-channel blocks of a group
     bool vec;     // states a multiple of four, a and the state 16-byte aligned
+    bool ranked;  // whole packed sequences: the longest first
     float *ws;    // split sequences: a record per item, see Record
 };
 
@@ -51,20 +52,21 @@ __device__ __forceinline__ float *record(const selective_scan_args &a, const Sca
     return k.ws + (long long)item * (a.states + 1) * a.channels;
 }
 
-constexpr int kMaxRanked = 256;  // sequences; more of them even out by themselves
+constexpr int kMaxRanked = 256;
 
 // The sequence that stands at place `rank` when the longest come first (ties by number), so
-// that the workgroups that start last are short (16384 ragged tokens x 4096 channels in 24
-// sequences: 349 us in their own order, 273 us so).
-__device__ __forceinline__ int by_length(const int *offsets, int nseq, int tokens, int rank, int &found) {
+// that the workgroups that start last are short (cut_prompt says when).
+// key: room for a sequence's length and number each.
+__device__ __forceinline__ int by_length(const int *offsets, int nseq, int tokens, int rank, uint64_t *key, int &found) {
     for (int i = threadIdx.x; i < nseq; i += blockDim.x) {
         const int len = clamped_offset(offsets, i + 1, tokens) - clamped_offset(offsets, i, tokens);
-        int before = 0, prev = clamped_offset(offsets, 0, tokens);
-        for (int j = 0; j < nseq; j++) {
-            const int next = clamped_offset(offsets, j + 1, tokens), other = next - prev;
-            before += other > len || (other == len && j < i);
-            prev = next;
-        }
+        key[i] = (uint64_t)max(len, 0) << 32 | (uint32_t)(nseq - i);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < nseq; i += blockDim.x) {
+        const uint64_t mine = key[i];
+        int before = 0;
+        for (int j = 0; j < nseq; j++) before += key[j] > mine;
         if (before == rank) found = i;
     }
     __syncthreads();
@@ -114,7 +116,8 @@ __global__ __launch_bounds__(64 * NW, NW <= 2 ? 4 : NW <= 8 ? 5 : NS == 4 ? 8 : 
     __shared__ int s_seq;
     __shared__ float2 s_d[TT][64];               // d, d * u
     __shared__ __attribute__((aligned(16))) float s_bc[2][TT][NP];
-    __shared__ float s_y[FIRST ? 1 : NW][FIRST ? 1 : TT][64];
+    __shared__ __attribute__((aligned(16))) float s_y[FIRST ? 1 : NW][FIRST ? 1 : TT][64];
+    static_assert(FIRST || sizeof(s_y) >= kMaxRanked * sizeof(uint64_t));
 
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int blocks = k.cblocks * a.groups;
@@ -127,8 +130,8 @@ __global__ __launch_bounds__(64 * NW, NW <= 2 ? 4 : NW <= 8 ? 5 : NS == 4 ? 8 : 
     SeqRun r;
     long long start = 0;
     if (a.offsets) {
-        if (!k.ws && a.nseq <= kMaxRanked) {
-            const int s = by_length(a.offsets, a.nseq, (int)a.tokens, item, s_seq);
+        if (!FIRST && k.ranked) {
+            const int s = by_length(a.offsets, a.nseq, (int)a.tokens, item, reinterpret_cast<uint64_t *>(s_y), s_seq);
             r.seq = s;
             r.start = clamped_offset(a.offsets, s, (int)a.tokens);
             const int e = clamped_offset(a.offsets, s + 1, (int)a.tokens);
@@ -503,6 +506,12 @@ ScanCut cut_prompt(const selective_scan_args &a, size_t ws_bytes, size_t *want) 
             if (*want && *want <= ws_bytes) k.run = (int)run;
         }
     }
+    // The order of lengths costs each workgroup a look at all of them, which long sequences earn
+    // back. Ordered and not, us, 16 states: 24 sequences of a mean of 683 tokens x 4096 channels 256
+    // and 297; 64 of 128 x 2048 71.4 and 92.0; 128 of 32 x 512 17.9 and 21.2, of 16 15.8 and 14.3; 256 of
+    // 128 x 2048 285 and 276, of 16 x 2048 88 and 68; 64 states, 256 of 128 x 512 288 and 339, of 16 112
+    // and 101.
+    k.ranked = a.offsets && k.run == kWhole && a.nseq <= kMaxRanked && 4 * a.tokens >= (long long)a.nseq * a.nseq;
     k.chunks = a.offsets ? 0 : (int)std::max((a.tokens + k.run - 1) / k.run, 1ll);  // empty sequences have a state
     k.items = a.offsets ? (int)(a.tokens / k.run + a.nseq) : k.chunks * a.nseq;
     return k;

@@ -122,3 +122,19 @@ def test_growth_past_a_chunk(d):
         y = c2d.selective_scan(*args, **kw, state=dev_state, workspace=workspace)
         ref.close(y.reshape(-1, d), want, bound, "y")
         ref.close(dev_state, state, state_bound, "state")
+
+
+@pytest.mark.parametrize("count,n,groups", [(70, 4, 1), (256, 4, 1), (256, 16, 2), (130, 64, 1)])
+def test_many_whole_sequences(count, n, groups):
+    """Sequences taken in the order of their lengths, equal and empty ones among them, in every number that is ordered."""
+    lengths = torch.randint(0, 140, (count,), generator=_rng(67)).tolist()
+    lengths[3] = lengths[count - 1] = max(lengths)
+    d = 32
+    assert 4 * sum(lengths) >= count * count
+    c = _scan_case(68, "f32", lengths, d, n, groups, {})
+    c["slots"] = torch.randperm(count + 2, generator=_rng(69))[:count].to(torch.int32)
+    want, bound, state, state_bound = _reference(c, lengths)
+    _, args, kw = _scan_args(c, lengths, True, {})
+    dev_state = _on(c["state"])
+    ref.close(c2d.selective_scan(*args, **kw, state=dev_state, workspace=False), want, bound, "y")
+    ref.close(dev_state, state, state_bound, "state")
