@@ -254,6 +254,10 @@ template <typename T, int NT, int MT, int W, int PER, bool ZEROS> hipError_t lau
 //    4096 x 4096      10.9 / 11.5  8.1 /  9.7  5.9 /  8.3  5.1 /  8.9  5.2 /  7.9  6.8 /  8.1
 //    2048 x 8192      17.4 / 17.9 12.3 / 14.5  8.6 / 12.0  6.5 / 12.4  7.3 / 11.4 10.3 / 12.1
 //    4096 x 1024       5.1 /  5.8  4.5 /  5.6  3.4 /  4.7  3.3 /  4.6  3.1 /  4.5  3.1 /  4.0
+// Past 16 rows the weights are read and decoded again for every 32 (one plan; not tuned). That
+// and the library's 1x1 convolution on 16-bit weights, us at 32 / 64 / 128 rows, groups of 64: 2048
+// -> 4096 8.1 / 8.2 / 14.3 and 15.4 / 15.6 / 15.8; 4096 -> 4096 12.0 / 12.3 / 22.5 and 17.1 / 17.8 / 22.0;
+// 2048 -> 16384 15.7 / 27.9 / 52.1 and 21.8 / 22.5 / 26.9; 8192 -> 32768 77 / 152 / 296 and 168 / 176 / 197.
 template <typename T, int PER, bool ZEROS> hipError_t launch_per(const matvec_w4_args &a, hipStream_t st) {
     const int n = (a.out_features + kTileN - 1) / kTileN, kb = (a.in_features + kTileK - 1) / kTileK;
     if (a.rows > 16) return launch<T, 2, 2, 8, PER, ZEROS>(a, st);

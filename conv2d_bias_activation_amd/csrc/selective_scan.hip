@@ -99,11 +99,15 @@ template <int NS> __device__ __forceinline__ void load_states(const float *row, 
 // The last tile stops at the chunk's end: a token of no step would not do there, as 0 * A is NaN
 // for an infinite A.
 // Bound by the vector ALU: 6 N issue slots of four cycles a token and channel, and about 38 for
-// the step size, gate, conversions and sums, against 4 values moved. Measured, bf16, 16
-// states: 16384 ragged tokens x 4096 channels 247 to 261 us, the ALUs 93 % busy; one sequence of
-// 32768 x 1024, in two passes, 231 to 235 us (85 %). Four states a lane on four waves are faster than eight
-// on two (the first case, at the time 273 and 396 us): more waves hide the latencies. At most
-// five waves a SIMD: registers for six spill to memory (261 us).
+// the step size, gate, conversions and sums (some 26 of them the formula's own), against 4
+// values moved. Measured, bf16, 16 states, boxes 4 % apart: 16384 ragged tokens x 4096 channels 256
+// to 267 us, the ALUs 93 % busy; one sequence of 32768 x 1024, in two passes, 236 us (86 %). Four
+// states a lane on four waves are faster than eight on two (267 and 381 us, 237 and 303): more
+// waves hide the latencies.
+// The bounds on a SIMD's waves: for 9 to 32 states five, as registers for six spill to memory
+// (267 and 276 us); for up to 8 four, as five spill (24 sequences of 16384 tokens x 4096 in all, 4
+// states: 376 and 559 us; 8 states 300 and 298). From 33 states on one workgroup of 16 waves fills
+// a CU, by its LDS up to 64 states and by its registers past that.
 template <typename T, int NS, int NW, bool FIRST>
 __global__ __launch_bounds__(64 * NW, NW <= 2 ? 4 : NW <= 8 ? 5 : NS == 4 ? 8 : 4) void scan_prompt_kernel(
     const selective_scan_args a, const ScanCut k) {
@@ -477,9 +481,10 @@ constexpr int kMaxChunks = 96;
 // How a prompt call is cut for a workspace of ws_bytes. A sequence left whole is walked by
 // one workgroup for each 64 channels, so its length is a time; a split one is read twice (the
 // first pass for the chunks' end states), 1.8 times the work, but fills the card. Whole and
-// split, us: 40 tokens x 512 channels 13.2 and 14.1, 64: 16.5 and 14.7, 100: 24.1 and 14.4.
+// split, us: 50 tokens x 512 channels x 16 states 11.0 and 12.5, 64: 12.1 and 12.8, 72: 13.5 and 12.6,
+// 100: 16.9 and 12.8; of 4 states 50: 14.9 and 14.3, 64: 17.1 and 14.6.
 // More chunks fill the card, but each reads the records before it: 32768 tokens x 1024 in 64
-// chunks 291 us, in 94 282 (then).
+// chunks 247 us, in 94 237.
 ScanCut cut_prompt(const selective_scan_args &a, size_t ws_bytes, size_t *want) {
     ScanCut k{};
     const int per = a.channels / a.groups;
@@ -494,9 +499,11 @@ ScanCut cut_prompt(const selective_scan_args &a, size_t ws_bytes, size_t *want) 
     // tokens a wave walks one after the other, whole and split over 1024 SIMDs
     const long long even = total * waves / 1024;
     if (longest > 48 && longest > even * 18 / 10 + 24) {
-        // five waves a SIMD are resident, and a chunk reads the records of those before it: whole
-        // tiles, two at least where there would be over 32 chunks (1000 tokens x 512 channels:
-        // 24.4 us in chunks of 16, 21.5 of 32; 400 tokens: 17.0 and 19.0)
+        // Chunks for five waves a SIMD, which is what the kernel of 9 to 32 states keeps (the others
+        // four: a quarter of their workgroups start late), in whole tiles; as a chunk reads
+        // the records of those before it, two tiles at least where there would be over 32
+        // chunks (1000 tokens x 512 channels: 22.7 us in chunks of 16, 19.2 of 32; 400 tokens:
+        // 15.5 and 16.8)
         const long long least = longest > 512 ? 16 : 0;
         const long long run = std::max({total * waves / (5 * 1024), longest / kMaxChunks, least}) / 16 * 16 + 16;
         if (run < longest) {

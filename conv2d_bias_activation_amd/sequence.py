@@ -5,7 +5,9 @@ token rows with 4-bit weights.
 As in the rest of the binding, PyTorch supplies device memory and streams, and everything is
 computed by the library's HIP kernels; this module checks tensors, fills the C structs and
 allocates outputs. Activations are channel-last, and a tensor may be a slice of a wider one
-(the columns of one projection), as long as the channels of a token are contiguous.
+(the columns of one projection), as long as the channels of a token are contiguous. ``out`` may
+be a slice too, but not of a tensor that holds an input: from its first to its last value it may
+not overlap one.
 
 A call on ``stream`` enqueues its work there (default: the device's current stream) and
 allocates what it returns there too; inputs made on another stream have to be waited for by

@@ -11,6 +11,9 @@
  *  - Activations are channel-last: the channels of one token are contiguous. Where a struct
  *    has strides (in elements), one token's row and one batch entry's first row may stand
  *    anywhere, so a slice of a wider projection is read in place. Strides may not be negative.
+ *    The output may not overlap an input or the state anywhere between its first and its last
+ *    value (CONV2D_EINVAL), so it is no slice of a tensor of which an input is another slice,
+ *    nor the residual.
  *  - Offsets into memory are 64-bit; a call may cover up to 2^30 tokens of up to 2^30 channels
  *    (inputs and outputs of a product, whose weights may number 2^40), and where it would
  *    need 2^32 GPU threads or more (many short sequences of many channels) it returns
@@ -123,7 +126,9 @@ int matvec_w4_pack(const void *codes, const void *scales, const void *zeros, voi
 
 /* y[r, o] = epilogue(sum_k x[r, k] * weight(o, k)) for `rows` token rows, the epilogue that of
  * conv2d_fused: bias, activation, and a residual before or after it. Sums are fp32. A row
- * of x with an infinity or NaN gives NaN. */
+ * of x with an infinity or NaN gives NaN. Made for the rows of single tokens: the weights are
+ * read again for every 32 rows, and from some 64 to 128 rows on conv2d_fused is faster, as a 1x1
+ * convolution with the weights' values in 16 bits. */
 typedef struct matvec_w4_args {
     const void *x;         /* [rows, in_features], rows x_row elements apart */
     const void *packed;    /* from matvec_w4_pack, with the same sizes, group, zeros and dtype */
