@@ -100,7 +100,7 @@ template <int NS> __device__ __forceinline__ void load_states(const float *row, 
 // for an infinite A.
 // Bound by the vector ALU: 6 N issue slots of four cycles a token and channel, and about 38 for
 // the step size, gate, conversions and sums (some 26 of them the formula's own), against 4
-// values moved. Measured, bf16, 16 states, boxes 4 % apart: 16384 ragged tokens x 4096 channels 256
+// values moved. Measured, bf16, 16 states, cards 4 % apart: 16384 ragged tokens x 4096 channels 256
 // to 267 us, the ALUs 93 % busy; one sequence of 32768 x 1024, in two passes, 236 us (86 %). Four
 // states a lane on four waves are faster than eight on two (267 and 381 us, 237 and 303): more
 // waves hide the latencies.
