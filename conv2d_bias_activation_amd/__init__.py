@@ -34,7 +34,8 @@ __all__ = ["conv2d_fused", "conv2d_fused_maxpool3x3s2", "maxpool3x3s2", "avgpool
            "workspace_size", "stack_workspace_size", "set_workspace", "DEFAULT_WORKSPACE_BYTES",
            "ACT_PRELU", "RES_BEFORE_ACT", "LAYOUT_NHWC", "LAYOUT_NCHW", "DTYPE_F32",
            "DTYPE_BF16", "DTYPE_F16", "causal_conv1d", "causal_conv1d_step", "selective_scan",
-           "selective_scan_step", "w4_pack", "matvec_w4", "W4Weights"]
+           "selective_scan_step", "gated_recurrence", "gated_recurrence_step", "gated_recurrence_backward",
+           "w4_pack", "matvec_w4", "W4Weights"]
 
 # Codes of include/conv2d_fused.h
 LAYOUT_NHWC, LAYOUT_NCHW = 0, 1
@@ -111,6 +112,11 @@ SEQUENCE_SIGNATURES = {
     "selective_scan": (_i, [_cp, _vp]),
     "selective_scan_workspace_size": (_i, [_cp, ctypes.POINTER(ctypes.c_size_t)]),
     "selective_scan_step": (_i, [_cp, _vp]),
+    "gated_recurrence": (_i, [_cp, _vp]),
+    "gated_recurrence_workspace_size": (_i, [_cp, ctypes.POINTER(ctypes.c_size_t)]),
+    "gated_recurrence_step": (_i, [_cp, _vp]),
+    "gated_recurrence_backward": (_i, [_cp, _vp]),
+    "gated_recurrence_backward_workspace_size": (_i, [_cp, ctypes.POINTER(ctypes.c_size_t)]),
     "matvec_w4_packed_bytes": (_i, [_i] * 4 + [ctypes.POINTER(ctypes.c_size_t)]),
     "matvec_w4_pack": (_i, [_vp] * 4 + [_i] * 4 + [_vp]),
     "matvec_w4": (_i, [_cp, _vp]),
@@ -796,5 +802,6 @@ def weights_to_ohwi(w, stream=None):
     return w2
 
 
-from .sequence import (W4Weights, causal_conv1d, causal_conv1d_step, matvec_w4, selective_scan,  # noqa: E402
+from .sequence import (W4Weights, causal_conv1d, causal_conv1d_step, gated_recurrence,  # noqa: E402
+                       gated_recurrence_backward, gated_recurrence_step, matvec_w4, selective_scan,
                        selective_scan_step, w4_pack)

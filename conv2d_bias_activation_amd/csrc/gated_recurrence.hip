@@ -1,0 +1,700 @@
+// Gated linear recurrence over channel-last token rows, for prompts and single tokens, and its
+// gradient (gfx950 only).
+//
+//     h_t = f_t h_{t-1} + b_t,   f = sigmoid(forget + bias),   b = (1 - f) x or x,   y = h silu(gate)
+//
+// A run of tokens maps the state before it to the state behind it as h -> A h + B, A the product
+// of its f and B what it ends in from zero; runs compose, so the waves of a workgroup take
+// neighbouring tokens of a tile, exchange their (A, B) in LDS and then know where each starts.
+// The gradient carried towards the first token, c_t = f_t g_t with g_t = e_t + c_{t+1} and e the
+// part of h_t's gradient that comes from y_t, is the same scan backwards: c -> A c + D.
+#include <algorithm>
+#include <initializer_list>
+
+#include "kernels.hpp"
+#include "runtime.hpp"
+#include "seq_common.hpp"
+
+namespace c2d {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// sigmoid(z) and 1 - sigmoid(z), both to full relative precision.
+__device__ __forceinline__ void gates(float z, float &keep, float &take) {
+    const float t = __builtin_amdgcn_exp2f(-fabsf(z) * kLog2e);
+    const float large = __builtin_amdgcn_rcpf(1.0f + t);
+    const float small = t * large;
+    keep = z >= 0.0f ? large : small;
+    take = z >= 0.0f ? small : large;
+}
+
+constexpr int kTW = 8;          // neighbouring tokens of a wave
+constexpr int kNW = 8;          // waves of a workgroup
+constexpr int kTile = kTW * kNW;
+constexpr int kWhole = 1 << 30;  // run of a call that is not split; whole tiles
+
+// How a prompt call is cut.
+struct RecCut {
+    int run;      // tokens of a chunk, whole tiles
+    int items;    // chunk numbers in all (find_run), or nseq * chunks
+    int chunks;   // unpacked: chunks of a sequence
+    int cblocks;  // blocks of 64 VEC channels
+    float *rec;   // split sequences: records of the chunks, [item][fields][channels]
+    float *tile;  // gradient: [tile number][2][channels]
+    float *bias;  // gradient: sums of grad_forget, [item][channels]
+};
+
+// Records of a split sequence's chunks, left by the first pass for the second.
+//   kA: product of f; 0 in the chunks from which the scan starts (see kB and kD)
+//   kB: end state, from zero; chunk 0: from the sequence's own start state. The last chunk's
+//       end state is of no use to another chunk; its place takes the sequence's start state
+//       (forward) or the gradient of its final state (backward), which the second pass
+//       cannot read from the state row any more, where another workgroup leaves the new one
+//   kD: gradient: carry at the chunk's first token, from zero; last chunk: from the final one
+enum { kA, kB, kD };
+
+// Where a workgroup stands.
+struct Place {
+    int chunk, last, item, end;  // number in the sequence, the last one's, in the call; end token
+    long long lead, start;       // batch entry; first row of the sequence
+    SeqRun r;
+};
+
+template <typename Args> __device__ __forceinline__ bool place_of(const Args &a, const RecCut &k, int item, Place &p) {
+    p.item = item;
+    p.start = 0;
+    if (a.offsets) {
+        if (!find_run(a.offsets, a.nseq, (int)a.tokens, k.run, item, &p.r)) return false;
+        p.start = p.r.start;
+    } else {
+        p.r.seq = item / k.chunks;
+        p.r.first = (item - p.r.seq * k.chunks) * k.run;
+        p.r.len = (int)a.tokens;
+        p.r.start = 0;
+    }
+    p.lead = a.offsets ? 0 : p.r.seq;
+    p.chunk = p.r.first / k.run;
+    p.last = p.r.len > 0 ? (p.r.len - 1) / k.run : 0;
+    p.end = min(p.r.len, p.r.first + k.run);
+    return true;
+}
+
+template <typename T> __device__ __forceinline__ const T *rows(const void *p, const Place &w, long long batch, long long token) {
+    return static_cast<const T *>(p) + w.lead * batch + w.start * token;
+}
+template <typename T> __device__ __forceinline__ T *rows(void *p, const Place &w, long long batch, long long token) {
+    return static_cast<T *>(p) + w.lead * batch + w.start * token;
+}
+
+template <int VEC> using Floats = Pack<float, VEC>;
+
+// kTW tokens from t on of token rows, the last row again from `end` on.
+template <typename T, int VEC>
+__device__ __forceinline__ void fetch(Pack<T, VEC> (&v)[kTW], const T *p, long long token, int t, int end, int c) {
+#pragma unroll
+    for (int i = 0; i < kTW; i++) v[i] = load_pack<T, VEC>(p + min(t + i, end - 1) * token + (unsigned)c);
+}
+
+// Composite of the records from lo on and before hi (towards later tokens, or earlier ones), the
+// waves taking parts of them.
+template <int VEC, bool BACK>
+__device__ __forceinline__ Floats<VEC> fold(const float *rec, long long stride, int channels, int lo, int hi, int c, int wave,
+                                            int lane, float2 (*s)[VEC][64]) {
+    const int per = (hi - lo + kNW - 1) / kNW, first = min(lo + wave * per, hi), n = min(per, hi - first);
+    float A[VEC], B[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; v++) A[v] = 1.0f, B[v] = 0.0f;
+    for (int j0 = 0; j0 < n; j0 += 4) {
+        Floats<VEC> ra[4], rb[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int j = min(j0 + i, n - 1);
+            const float *p = rec + (BACK ? first + n - 1 - j : first + j) * stride + c;
+            ra[i] = load_pack<float, VEC>(p + kA * (long long)channels);
+            rb[i] = load_pack<float, VEC>(p + (BACK ? kD : kB) * (long long)channels);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            if (j0 + i >= n) break;
+#pragma unroll
+            for (int v = 0; v < VEC; v++) {
+                B[v] = fmaf(ra[i].v[v], B[v], rb[i].v[v]);
+                A[v] *= ra[i].v[v];
+            }
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; v++) s[wave][v][lane] = float2{A[v], B[v]};
+    __syncthreads();
+    Floats<VEC> out{};
+#pragma unroll
+    for (int w = 0; w < kNW; w++)
+#pragma unroll
+        for (int v = 0; v < VEC; v++) {
+            const float2 m = s[BACK ? kNW - 1 - w : w][v][lane];
+            out.v[v] = fmaf(m.x, out.v[v], m.y);
+        }
+    __syncthreads();
+    return out;
+}
+
+// ---------------------------------------------------------------------------- prompts
+
+// FIRST: the first pass over split sequences, which leaves the chunks' records; else the pass
+// that writes y and the states.
+template <typename T, int VEC, bool FIRST>
+__global__ __launch_bounds__(64 * kNW) void rec_prompt_kernel(const gated_recurrence_args a, const RecCut k) {
+    __shared__ float2 s_run[2][kNW][VEC][64];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    // the second pass takes the chunks that the first read last first: they may still be cached
+    const int item = FIRST ? blockIdx.x / k.cblocks : k.items - 1 - blockIdx.x / k.cblocks;
+    const int ch = (int)(blockIdx.x % k.cblocks) * 64 * VEC + lane * VEC;
+    const bool on = ch < a.channels;
+    const int c = on ? ch : a.channels - VEC;
+    Place p;
+    if (!place_of(a, k, item, p)) return;
+    if (FIRST && p.chunk == p.last) return;
+
+    const T *x = rows<T>(a.x, p, a.x_batch, a.x_token), *forget = rows<T>(a.forget, p, a.forget_batch, a.forget_token);
+    const T *gate = a.gate ? rows<T>(a.gate, p, a.gate_batch, a.gate_token) : nullptr;
+    T *y = rows<T>(a.y, p, a.y_batch, a.y_token);
+    const int row = state_row(a.state, a.slots, p.r.seq, a.state_rows);
+    float *state = row < 0 ? nullptr : a.state + (long long)row * a.channels + c;
+    const long long stride = 2ll * a.channels;
+
+    Floats<VEC> bias{}, h{};
+    if (a.forget_bias) bias = load_pack<float, VEC>(a.forget_bias + c);
+    if (p.chunk == 0 && (FIRST || p.last == 0) && state && !a.fresh) h = load_pack<float, VEC>(state);
+    if (FIRST && p.chunk == 0 && wave == 0 && on)
+        store_pack<float, VEC>(k.rec + (item + p.last) * stride + kB * (long long)a.channels + c, h);
+
+    Pack<T, VEC> nx[kTW], nf[kTW], ng[kTW];
+    auto next = [&](int t0) {
+        const int t = t0 + wave * kTW;
+        fetch<T, VEC>(nx, x, a.x_token, t, p.end, c);
+        fetch<T, VEC>(nf, forget, a.forget_token, t, p.end, c);
+        if (!FIRST && gate) fetch<T, VEC>(ng, gate, a.gate_token, t, p.end, c);
+    };
+    if (p.end > p.r.first) next(p.r.first);
+    if (!FIRST && p.last > 0) {
+        const float *rec = k.rec + (item - p.chunk) * stride;
+        if (p.chunk == 0)
+            h = load_pack<float, VEC>(rec + p.last * stride + kB * (long long)a.channels + c);
+        else
+            h = fold<VEC, false>(rec, stride, a.channels, 0, p.chunk, c, wave, lane, s_run[0]);
+    }
+    float decay[VEC];  // FIRST: of the chunk so far
+#pragma unroll
+    for (int v = 0; v < VEC; v++) decay[v] = 1.0f;
+
+    int buf = 0;
+    for (int t0 = p.r.first; t0 < p.end; t0 += kTile, buf ^= 1) {
+        const int t = t0 + wave * kTW;
+        float f[kTW][VEC], b[kTW][VEC], z[kTW][VEC], A[VEC], B[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; v++) A[v] = 1.0f, B[v] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kTW; i++) {
+#pragma unroll
+            for (int v = 0; v < VEC; v++) {
+                float take;
+                gates(to_f32(nf[i].v[v]) + bias.v[v], f[i][v], take);
+                b[i][v] = to_f32(nx[i].v[v]) * (a.coupled ? take : 1.0f);
+                if (t + i >= p.end) f[i][v] = 1.0f, b[i][v] = 0.0f;
+                B[v] = fmaf(f[i][v], B[v], b[i][v]);
+                A[v] *= f[i][v];
+                if (!FIRST) z[i][v] = gate ? activate_c<CONV2D_ACT_SILU>(to_f32(ng[i].v[v]), 0.0f) : 1.0f;
+            }
+        }
+        if (t0 + kTile < p.end) next(t0 + kTile);
+#pragma unroll
+        for (int v = 0; v < VEC; v++) s_run[buf][wave][v][lane] = float2{A[v], B[v]};
+        __syncthreads();
+        float from[VEC];  // the wave's start state
+#pragma unroll
+        for (int w = 0; w < kNW; w++)
+#pragma unroll
+            for (int v = 0; v < VEC; v++) {
+                if (w == wave) from[v] = h.v[v];
+                const float2 m = s_run[buf][w][v][lane];
+                h.v[v] = fmaf(m.x, h.v[v], m.y);
+                if (FIRST) decay[v] *= m.x;
+            }
+        if (FIRST) continue;
+#pragma unroll
+        for (int i = 0; i < kTW; i++) {
+            Pack<T, VEC> out;
+#pragma unroll
+            for (int v = 0; v < VEC; v++) {
+                from[v] = fmaf(f[i][v], from[v], b[i][v]);
+                out.v[v] = round_fp32<T>(from[v] * z[i][v]);
+            }
+            if (on && t + i < p.end) store_pack<T, VEC>(y + (t + i) * a.y_token + (unsigned)c, out);
+        }
+    }
+    if (!on || wave != 0) return;
+    if (FIRST) {
+        float *q = k.rec + item * stride + c;
+        Floats<VEC> A;
+#pragma unroll
+        for (int v = 0; v < VEC; v++) A.v[v] = p.chunk == 0 ? 0.0f : decay[v];
+        store_pack<float, VEC>(q + kA * (long long)a.channels, A);
+        store_pack<float, VEC>(q + kB * (long long)a.channels, h);
+    } else if (state && p.chunk == p.last) {
+        store_pack<float, VEC>(state, h);
+    }
+}
+
+// ---------------------------------------------------------------------------- gradient
+
+// The first pass of the gradient walks forwards: it leaves, for each tile, the state before it as
+// an affine map of the state before the chunk, and, for split sequences, the chunks' records.
+template <typename T, int VEC>
+__global__ __launch_bounds__(64 * kNW) void rec_back_first_kernel(const gated_recurrence_backward_args a, const RecCut k) {
+    __shared__ float4 s_run[2][kNW][VEC][64];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int item = blockIdx.x / k.cblocks;
+    const int ch = (int)(blockIdx.x % k.cblocks) * 64 * VEC + lane * VEC;
+    const bool on = ch < a.channels;
+    const int c = on ? ch : a.channels - VEC;
+    Place p;
+    if (!place_of(a, k, item, p)) return;
+    const bool split = p.last > 0;
+
+    const T *x = rows<T>(a.x, p, a.x_batch, a.x_token), *forget = rows<T>(a.forget, p, a.forget_batch, a.forget_token);
+    const T *gate = a.gate ? rows<T>(a.gate, p, a.gate_batch, a.gate_token) : nullptr;
+    const T *grad = rows<T>(a.grad, p, a.grad_batch, a.grad_token);
+    const long long tiles = a.offsets ? 0 : (a.tokens + kTile - 1) / kTile;
+    float *tile = k.tile + (a.offsets ? p.start / kTile + p.r.seq : p.r.seq * tiles) * 2 * a.channels + c;
+
+    Floats<VEC> bias{}, h{}, carry{};
+    if (a.forget_bias) bias = load_pack<float, VEC>(a.forget_bias + c);
+    if (p.chunk == 0) {
+        const int row = state_row(a.state, a.slots, p.r.seq, a.state_rows);
+        if (row >= 0) h = load_pack<float, VEC>(a.state + (long long)row * a.channels + c);
+    }
+    if (split && p.chunk == p.last) {
+        const int row = state_row(a.grad_state, a.slots, p.r.seq, a.state_rows);
+        if (row >= 0) carry = load_pack<float, VEC>(a.grad_state + (long long)row * a.channels + c);
+    }
+    Pack<T, VEC> nx[kTW], nf[kTW], ng[kTW], ne[kTW];
+    auto next = [&](int t0) {
+        const int t = t0 + wave * kTW;
+        fetch<T, VEC>(nx, x, a.x_token, t, p.end, c);
+        fetch<T, VEC>(nf, forget, a.forget_token, t, p.end, c);
+        if (split) {
+            fetch<T, VEC>(ne, grad, a.grad_token, t, p.end, c);
+            if (gate) fetch<T, VEC>(ng, gate, a.gate_token, t, p.end, c);
+        }
+    };
+    if (p.end > p.r.first) next(p.r.first);
+    float decay[VEC], D[VEC];  // of the chunk so far
+#pragma unroll
+    for (int v = 0; v < VEC; v++) decay[v] = 1.0f, D[v] = 0.0f;
+
+    int buf = 0;
+    for (int t0 = p.r.first; t0 < p.end; t0 += kTile, buf ^= 1) {
+        if (wave == 0 && on) {
+            float *q = tile + (t0 / kTile) * 2ll * a.channels;
+            Floats<VEC> A;
+#pragma unroll
+            for (int v = 0; v < VEC; v++) A.v[v] = p.chunk == 0 ? 0.0f : decay[v];
+            store_pack<float, VEC>(q, A);
+            store_pack<float, VEC>(q + a.channels, h);
+        }
+        const int t = t0 + wave * kTW;
+        float A[VEC], B[VEC], E[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; v++) A[v] = 1.0f, B[v] = 0.0f, E[v] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kTW; i++) {
+#pragma unroll
+            for (int v = 0; v < VEC; v++) {
+                float f, take;
+                gates(to_f32(nf[i].v[v]) + bias.v[v], f, take);
+                float b = to_f32(nx[i].v[v]) * (a.coupled ? take : 1.0f);
+                if (t + i >= p.end) f = 1.0f, b = 0.0f;
+                B[v] = fmaf(f, B[v], b);
+                A[v] *= f;
+                if (split) {
+                    float e = to_f32(ne[i].v[v]);
+                    if (gate) e *= activate_c<CONV2D_ACT_SILU>(to_f32(ng[i].v[v]), 0.0f);
+                    if (t + i >= p.end) e = 0.0f;
+                    E[v] = fmaf(A[v], e, E[v]);
+                }
+            }
+        }
+        if (t0 + kTile < p.end) next(t0 + kTile);
+#pragma unroll
+        for (int v = 0; v < VEC; v++) s_run[buf][wave][v][lane] = float4{A[v], B[v], E[v], 0.0f};
+        __syncthreads();
+        if (wave != 0) continue;
+#pragma unroll
+        for (int w = 0; w < kNW; w++)
+#pragma unroll
+            for (int v = 0; v < VEC; v++) {
+                const float4 m = s_run[buf][w][v][lane];
+                h.v[v] = fmaf(m.x, h.v[v], m.y);
+                D[v] = fmaf(decay[v], m.z, D[v]);
+                decay[v] *= m.x;
+            }
+    }
+    if (!split || !on || wave != 0) return;
+    float *q = k.rec + item * 3ll * a.channels + c;
+    Floats<VEC> A, B, E;
+    const bool last = p.chunk == p.last;
+#pragma unroll
+    for (int v = 0; v < VEC; v++) {
+        A.v[v] = p.chunk == 0 || last ? 0.0f : decay[v];
+        B.v[v] = last ? carry.v[v] : h.v[v];
+        E.v[v] = last ? fmaf(decay[v], carry.v[v], D[v]) : D[v];
+    }
+    store_pack<float, VEC>(q + kA * (long long)a.channels, A);
+    store_pack<float, VEC>(q + kB * (long long)a.channels, B);
+    store_pack<float, VEC>(q + kD * (long long)a.channels, E);
+}
+
+// The second pass walks backwards over the tiles and writes the gradients.
+template <typename T, int VEC>
+__global__ __launch_bounds__(64 * kNW) void rec_back_kernel(const gated_recurrence_backward_args a, const RecCut k) {
+    __shared__ float4 s_run[2][kNW][VEC][64];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int item = k.items - 1 - blockIdx.x / k.cblocks;
+    const int ch = (int)(blockIdx.x % k.cblocks) * 64 * VEC + lane * VEC;
+    const bool on = ch < a.channels;
+    const int c = on ? ch : a.channels - VEC;
+    float sum[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; v++) sum[v] = 0.0f;
+    Place p;
+    if (!place_of(a, k, item, p)) {
+        if (k.bias && wave == 0 && on) store_pack<float, VEC>(k.bias + item * (long long)a.channels + c, Floats<VEC>{});
+        return;
+    }
+    const T *x = rows<T>(a.x, p, a.x_batch, a.x_token), *forget = rows<T>(a.forget, p, a.forget_batch, a.forget_token);
+    const T *gate = a.gate ? rows<T>(a.gate, p, a.gate_batch, a.gate_token) : nullptr;
+    const T *grad = rows<T>(a.grad, p, a.grad_batch, a.grad_token);
+    T *gx = rows<T>(a.grad_x, p, a.grad_x_batch, a.grad_x_token);
+    T *gf = rows<T>(a.grad_forget, p, a.grad_forget_batch, a.grad_forget_token);
+    T *gg = a.gate ? rows<T>(a.grad_gate, p, a.grad_gate_batch, a.grad_gate_token) : nullptr;
+    const long long tiles = a.offsets ? 0 : (a.tokens + kTile - 1) / kTile;
+    const float *tile = k.tile + (a.offsets ? p.start / kTile + p.r.seq : p.r.seq * tiles) * 2 * a.channels + c;
+    const int row = state_row(a.grad_state, a.slots, p.r.seq, a.state_rows);
+    float *grad_state = row < 0 ? nullptr : a.grad_state + (long long)row * a.channels + c;
+
+    Floats<VEC> bias{}, before{}, carry{};  // state before the chunk, gradient carried into the tile
+    if (a.forget_bias) bias = load_pack<float, VEC>(a.forget_bias + c);
+
+    Pack<T, VEC> nx[kTW], nf[kTW], ng[kTW], ne[kTW];
+    Floats<VEC> na, nb;
+    auto next = [&](int t0) {
+        const int t = t0 + wave * kTW;
+        const float *q = tile + (t0 / kTile) * 2ll * a.channels;
+        na = load_pack<float, VEC>(q);
+        nb = load_pack<float, VEC>(q + a.channels);
+        fetch<T, VEC>(nx, x, a.x_token, t, p.end, c);
+        fetch<T, VEC>(nf, forget, a.forget_token, t, p.end, c);
+        fetch<T, VEC>(ne, grad, a.grad_token, t, p.end, c);
+        if (gate) fetch<T, VEC>(ng, gate, a.gate_token, t, p.end, c);
+    };
+    const int final = p.end > p.r.first ? p.r.first + (p.end - 1 - p.r.first) / kTile * kTile : p.r.first - kTile;
+    if (final >= p.r.first) next(final);
+    if (p.last > 0) {
+        const float *rec = k.rec + (item - p.chunk) * 3ll * a.channels;
+        float2(*s)[VEC][64] = reinterpret_cast<float2(*)[VEC][64]>(s_run);
+        if (p.chunk > 0) before = fold<VEC, false>(rec, 3ll * a.channels, a.channels, 0, p.chunk, c, wave, lane, s);
+        if (p.chunk < p.last)
+            carry = fold<VEC, true>(rec, 3ll * a.channels, a.channels, p.chunk + 1, p.last + 1, c, wave, lane, s);
+        else
+            carry = load_pack<float, VEC>(rec + p.last * 3ll * a.channels + kB * (long long)a.channels + c);
+    } else if (grad_state) {
+        carry = load_pack<float, VEC>(grad_state);
+    }
+
+    int buf = 0;
+    for (int t0 = final; t0 >= p.r.first; t0 -= kTile, buf ^= 1) {
+        const int t = t0 + wave * kTW;
+        float xs[kTW][VEC], f[kTW][VEC], take[kTW][VEC], e[kTW][VEC], dz[kTW][VEC], A[VEC], B[VEC], D[VEC];
+        float start[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; v++) {
+            A[v] = 1.0f, B[v] = 0.0f, D[v] = 0.0f;
+            start[v] = fmaf(na.v[v], before.v[v], nb.v[v]);
+        }
+#pragma unroll
+        for (int i = 0; i < kTW; i++) {
+#pragma unroll
+            for (int v = 0; v < VEC; v++) {
+                xs[i][v] = to_f32(nx[i].v[v]);
+                gates(to_f32(nf[i].v[v]) + bias.v[v], f[i][v], take[i][v]);
+                e[i][v] = to_f32(ne[i].v[v]);
+                dz[i][v] = 0.0f;
+                if (gate) {
+                    const float g = to_f32(ng[i].v[v]);
+                    float up, down;
+                    gates(g, up, down);
+                    dz[i][v] = e[i][v] * up * fmaf(g, down, 1.0f);
+                    e[i][v] *= g * up;
+                }
+                if (t + i >= p.end) f[i][v] = 1.0f, xs[i][v] = 0.0f, e[i][v] = 0.0f;
+                const float b = xs[i][v] * (a.coupled ? take[i][v] : 1.0f);
+                B[v] = fmaf(f[i][v], B[v], b);
+                D[v] = fmaf(A[v] * f[i][v], e[i][v], D[v]);
+                A[v] *= f[i][v];
+            }
+        }
+        if (t0 > p.r.first) next(t0 - kTile);
+#pragma unroll
+        for (int v = 0; v < VEC; v++) s_run[buf][wave][v][lane] = float4{A[v], B[v], D[v], 0.0f};
+        __syncthreads();
+        float h[VEC], cin[VEC];  // state before the wave's tokens, carry behind them
+#pragma unroll
+        for (int w = 0; w < kNW; w++)
+#pragma unroll
+            for (int v = 0; v < VEC; v++) {
+                if (w == wave) h[v] = start[v];
+                const float4 m = s_run[buf][w][v][lane];
+                start[v] = fmaf(m.x, start[v], m.y);
+            }
+#pragma unroll
+        for (int w = kNW - 1; w >= 0; w--)
+#pragma unroll
+            for (int v = 0; v < VEC; v++) {
+                if (w == wave) cin[v] = carry.v[v];
+                const float4 m = s_run[buf][w][v][lane];
+                carry.v[v] = fmaf(m.x, carry.v[v], m.z);
+            }
+        float prev[kTW][VEC];  // states before each token
+#pragma unroll
+        for (int i = 0; i < kTW; i++)
+#pragma unroll
+            for (int v = 0; v < VEC; v++) {
+                prev[i][v] = h[v];
+                h[v] = fmaf(f[i][v], h[v], xs[i][v] * (a.coupled ? take[i][v] : 1.0f));
+                dz[i][v] *= h[v];
+            }
+#pragma unroll
+        for (int i = kTW - 1; i >= 0; i--) {
+            Pack<T, VEC> ox, of, og;
+#pragma unroll
+            for (int v = 0; v < VEC; v++) {
+                const float g = e[i][v] + cin[v];
+                const float d = g * f[i][v] * take[i][v] * (a.coupled ? prev[i][v] - xs[i][v] : prev[i][v]);
+                ox.v[v] = round_fp32<T>(a.coupled ? g * take[i][v] : g);
+                of.v[v] = round_fp32<T>(d);
+                og.v[v] = round_fp32<T>(dz[i][v]);
+                cin[v] = g * f[i][v];
+                if (t + i < p.end) sum[v] += d;
+            }
+            if (on && t + i < p.end) {
+                store_pack<T, VEC>(gx + (t + i) * a.grad_x_token + (unsigned)c, ox);
+                store_pack<T, VEC>(gf + (t + i) * a.grad_forget_token + (unsigned)c, of);
+                if (gate) store_pack<T, VEC>(gg + (t + i) * a.grad_gate_token + (unsigned)c, og);
+            }
+        }
+    }
+    if (k.bias) {
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < VEC; v++) s_run[0][wave][v][lane].x = sum[v];
+        __syncthreads();
+        if (wave == 0 && on) {
+            Floats<VEC> total{};
+#pragma unroll
+            for (int w = 0; w < kNW; w++)
+#pragma unroll
+                for (int v = 0; v < VEC; v++) total.v[v] += s_run[0][w][v][lane].x;
+            store_pack<float, VEC>(k.bias + item * (long long)a.channels + c, total);
+        }
+    }
+    if (on && wave == 0 && grad_state && p.chunk == 0) store_pack<float, VEC>(grad_state, carry);
+}
+
+// Sums of `items` rows of partial sums, in a fixed order.
+__global__ __launch_bounds__(1024) void rec_bias_kernel(const float *part, float *out, int items, int channels) {
+    __shared__ float s[16][64];
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int c = blockIdx.x * 64 + lane, at = min(c, channels - 1);
+    float sum = 0.0f;
+    for (int i = wave; i < items; i += 16) sum += part[i * (long long)channels + at];
+    s[wave][lane] = sum;
+    __syncthreads();
+    if (wave || c >= channels) return;
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 16; w++) sum += s[w][lane];
+    out[c] = sum;
+}
+
+// ---------------------------------------------------------------------------- single tokens
+
+constexpr int kBlock = 256;
+
+// One token of each sequence, VEC channels a thread.
+template <typename T, int VEC>
+__global__ __launch_bounds__(kBlock) void rec_token_kernel(const gated_recurrence_args a, int cblocks) {
+    const int c = ((int)(blockIdx.x % cblocks) * kBlock + threadIdx.x) * VEC;
+    const long long seq = blockIdx.x / cblocks;
+    if (c >= a.channels) return;
+    const int row = state_row(a.state, a.slots, (int)seq, a.state_rows);
+    float *state = row < 0 ? nullptr : a.state + (long long)row * a.channels + c;
+    const Pack<T, VEC> x = load_pack<T, VEC>((const T *)a.x + seq * a.x_token + c);
+    const Pack<T, VEC> z = load_pack<T, VEC>((const T *)a.forget + seq * a.forget_token + c);
+    Pack<T, VEC> gate{}, y;
+    Floats<VEC> bias{}, h{};
+    if (a.gate) gate = load_pack<T, VEC>((const T *)a.gate + seq * a.gate_token + c);
+    if (a.forget_bias) bias = load_pack<float, VEC>(a.forget_bias + c);
+    if (state && !a.fresh) h = load_pack<float, VEC>(state);
+#pragma unroll
+    for (int v = 0; v < VEC; v++) {
+        float keep, take;
+        gates(to_f32(z.v[v]) + bias.v[v], keep, take);
+        h.v[v] = fmaf(keep, h.v[v], to_f32(x.v[v]) * (a.coupled ? take : 1.0f));
+        y.v[v] = round_fp32<T>(a.gate ? h.v[v] * activate_c<CONV2D_ACT_SILU>(to_f32(gate.v[v]), 0.0f) : h.v[v]);
+    }
+    if (state) store_pack<float, VEC>(state, h);
+    store_pack<T, VEC>((T *)a.y + seq * a.y_token + c, y);
+}
+
+template <typename T, int VEC> hipError_t launch_token(const gated_recurrence_args &a, hipStream_t st) {
+    const int cblocks = (a.channels + kBlock * VEC - 1) / (kBlock * VEC);
+    return launch_blocks(rec_token_kernel<T, VEC>, (long long)cblocks * a.nseq, kBlock, st, a, cblocks);
+}
+
+// ---------------------------------------------------------------------------- host
+
+struct Reach {
+    const void *p;
+    long long batch, token;
+};
+
+// Whether groups of `vec` channels of every row stand at whole multiples of their size.
+bool grouped(int vec, int eb, int channels, bool batches, std::initializer_list<Reach> rows, std::initializer_list<const float *> floats) {
+    if (channels % vec) return false;
+    for (const Reach &r : rows)
+        if (r.p && ((uintptr_t)r.p % (vec * eb) || r.token % vec || (batches && r.batch % vec))) return false;
+    for (const float *p : floats)
+        if ((uintptr_t)p % (4 * vec)) return false;
+    return true;
+}
+
+int vec_of(const gated_recurrence_args &a) {
+    const bool batches = !a.offsets;
+    const int vec = a.dtype == CONV2D_DTYPE_F32 ? 1 : 2;
+    return grouped(vec, 4 / vec, a.channels, batches,
+                   {{a.x, a.x_batch, a.x_token}, {a.forget, a.forget_batch, a.forget_token}, {a.gate, a.gate_batch, a.gate_token},
+                    {a.y, a.y_batch, a.y_token}},
+                   {a.forget_bias, a.state}) ? vec : 1;
+}
+
+int vec_of(const gated_recurrence_backward_args &a) {
+    const bool batches = !a.offsets;
+    const int vec = a.dtype == CONV2D_DTYPE_F32 ? 1 : 2;
+    return grouped(vec, 4 / vec, a.channels, batches,
+                   {{a.grad, a.grad_batch, a.grad_token}, {a.x, a.x_batch, a.x_token}, {a.forget, a.forget_batch, a.forget_token},
+                    {a.gate, a.gate_batch, a.gate_token}, {a.grad_x, a.grad_x_batch, a.grad_x_token},
+                    {a.grad_forget, a.grad_forget_batch, a.grad_forget_token}, {a.grad_gate, a.grad_gate_batch, a.grad_gate_token}},
+                   {a.forget_bias, a.state, a.grad_state}) ? vec : 1;
+}
+
+// Chunks for some 1024 workgroups. *longest: a bound of the tokens of the longest sequence.
+template <typename Args> RecCut cut(const Args &a, int vec, bool split) {
+    RecCut k{};
+    k.cblocks = (a.channels + 64 * vec - 1) / (64 * vec);
+    const long long total = a.offsets ? a.tokens : a.tokens * a.nseq;
+    long long longest = a.offsets ? (a.longest ? a.longest : 2 * (total / std::max(a.nseq, 1))) : a.tokens;
+    if (longest > a.tokens) longest = a.tokens;
+    k.run = kWhole;
+    if (split) {
+        const long long run = (total * k.cblocks / 1024 + kTile - 1) / kTile * kTile;
+        const long long least = 2 * kTile;
+        if (std::max(run, least) < longest) k.run = (int)std::max(run, least);
+    }
+    k.chunks = a.offsets ? 0 : (int)std::max((a.tokens + k.run - 1) / k.run, 1ll);
+    k.items = a.offsets ? (int)(a.tokens / k.run + a.nseq) : k.chunks * a.nseq;
+    return k;
+}
+
+size_t record_bytes(const RecCut &k, int fields, int channels) {
+    return k.run < kWhole ? ((size_t)k.items * fields * channels * 4 + 255) / 256 * 256 : 0;
+}
+
+template <typename T, int VEC> hipError_t launch_prompt(const gated_recurrence_args &a, const RecCut &k, hipStream_t st) {
+    const long long blocks = (long long)k.items * k.cblocks;
+    if (k.rec) {
+        const hipError_t e = launch_blocks(rec_prompt_kernel<T, VEC, true>, blocks, 64 * kNW, st, a, k);
+        if (e != hipSuccess) return e;
+    }
+    return launch_blocks(rec_prompt_kernel<T, VEC, false>, blocks, 64 * kNW, st, a, k);
+}
+
+template <typename T, int VEC> hipError_t launch_back(const gated_recurrence_backward_args &a, const RecCut &k, hipStream_t st) {
+    const long long blocks = (long long)k.items * k.cblocks;
+    hipError_t e = hipSuccess;
+    if (blocks) e = launch_blocks(rec_back_first_kernel<T, VEC>, blocks, 64 * kNW, st, a, k);
+    if (blocks && e == hipSuccess) e = launch_blocks(rec_back_kernel<T, VEC>, blocks, 64 * kNW, st, a, k);
+    if (e == hipSuccess && a.grad_forget_bias)
+        e = launch_blocks(rec_bias_kernel, (a.channels + 63) / 64, 1024, st, k.bias, a.grad_forget_bias, k.items, a.channels);
+    return e;
+}
+
+struct BackLayout {
+    RecCut k;
+    size_t rec, tile, bias, bytes;
+};
+
+BackLayout back_layout(const gated_recurrence_backward_args &a) {
+    BackLayout l{};
+    l.k = cut(a, vec_of(a), true);
+    l.rec = record_bytes(l.k, 3, a.channels);
+    const long long tiles = a.offsets ? a.tokens / kTile + a.nseq : (a.tokens + kTile - 1) / kTile * a.nseq;
+    l.tile = ((size_t)tiles * 2 * a.channels * 4 + 255) / 256 * 256;
+    l.bias = a.grad_forget_bias ? (size_t)l.k.items * a.channels * 4 : 0;
+    l.bytes = l.rec + l.tile + l.bias;
+    return l;
+}
+
+}  // namespace
+
+size_t recurrence_workspace(const gated_recurrence_args &a) { return record_bytes(cut(a, vec_of(a), true), 2, a.channels); }
+
+hipError_t launch_recurrence(const gated_recurrence_args &a, void *ws, size_t ws_bytes, hipStream_t st) {
+    const int vec = vec_of(a);
+    RecCut k = cut(a, vec, true);
+    const size_t want = record_bytes(k, 2, a.channels);
+    if (want && ws && want <= ws_bytes)
+        k.rec = static_cast<float *>(ws);
+    else
+        k = cut(a, vec, false);
+    if (a.dtype == CONV2D_DTYPE_F32) return launch_prompt<float, 1>(a, k, st);
+    if (a.dtype == CONV2D_DTYPE_BF16) return vec == 2 ? launch_prompt<bf16, 2>(a, k, st) : launch_prompt<bf16, 1>(a, k, st);
+    return vec == 2 ? launch_prompt<f16, 2>(a, k, st) : launch_prompt<f16, 1>(a, k, st);
+}
+
+hipError_t launch_recurrence_token(const gated_recurrence_args &a, hipStream_t st) {
+    const int vec = a.dtype == CONV2D_DTYPE_F32 ? 4 : 8;
+    const bool whole = a.channels % vec == 0 && aligned16(a.x) && aligned16(a.forget) && aligned16(a.gate) && aligned16(a.y) &&
+                       a.x_token % vec == 0 && a.forget_token % vec == 0 && (!a.gate || a.gate_token % vec == 0) &&
+                       a.y_token % vec == 0 && aligned16(a.forget_bias) && aligned16(a.state);
+    if (a.dtype == CONV2D_DTYPE_F32) return whole ? launch_token<float, 4>(a, st) : launch_token<float, 1>(a, st);
+    if (a.dtype == CONV2D_DTYPE_BF16) return whole ? launch_token<bf16, 8>(a, st) : launch_token<bf16, 1>(a, st);
+    return whole ? launch_token<f16, 8>(a, st) : launch_token<f16, 1>(a, st);
+}
+
+size_t recurrence_backward_workspace(const gated_recurrence_backward_args &a) { return back_layout(a).bytes; }
+
+hipError_t launch_recurrence_backward(const gated_recurrence_backward_args &a, void *ws, hipStream_t st) {
+    BackLayout l = back_layout(a);
+    char *p = static_cast<char *>(ws);
+    if (l.rec) l.k.rec = reinterpret_cast<float *>(p);
+    l.k.tile = reinterpret_cast<float *>(p + l.rec);
+    if (a.grad_forget_bias) l.k.bias = reinterpret_cast<float *>(p + l.rec + l.tile);
+    const int vec = vec_of(a);
+    if (a.dtype == CONV2D_DTYPE_F32) return launch_back<float, 1>(a, l.k, st);
+    if (a.dtype == CONV2D_DTYPE_BF16) return vec == 2 ? launch_back<bf16, 2>(a, l.k, st) : launch_back<bf16, 1>(a, l.k, st);
+    return vec == 2 ? launch_back<f16, 2>(a, l.k, st) : launch_back<f16, 1>(a, l.k, st);
+}
+
+}  // namespace c2d

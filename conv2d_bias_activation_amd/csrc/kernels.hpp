@@ -234,6 +234,11 @@ hipError_t launch_causal_conv(const causal_conv1d_args &a, bool vec, bool step, 
 size_t scan_workspace(const selective_scan_args &a);  // bytes that its preferred split wants
 hipError_t launch_scan(const selective_scan_args &a, void *ws, size_t ws_bytes, hipStream_t st);
 hipError_t launch_scan_token(const selective_scan_args &a, hipStream_t st);
+size_t recurrence_workspace(const gated_recurrence_args &a);  // bytes that its preferred split wants
+hipError_t launch_recurrence(const gated_recurrence_args &a, void *ws, size_t ws_bytes, hipStream_t st);
+hipError_t launch_recurrence_token(const gated_recurrence_args &a, hipStream_t st);
+size_t recurrence_backward_workspace(const gated_recurrence_backward_args &a);  // bytes that it needs
+hipError_t launch_recurrence_backward(const gated_recurrence_backward_args &a, void *ws, hipStream_t st);
 size_t w4_packed_bytes(int out_features, int in_features, int group, bool zeros);
 hipError_t launch_w4_pack(const void *codes, const void *scales, const void *zeros, void *packed, int out_features,
                           int in_features, int group, int dtype, hipStream_t st);

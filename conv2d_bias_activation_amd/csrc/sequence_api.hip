@@ -203,6 +203,98 @@ int run_scan(const selective_scan_args *args, bool step, void *stream) {
     return launched(op, step ? launch_scan_token(*args, st) : launch_scan(*args, ws.p, ws.bytes, st));
 }
 
+// Validates a recurrence's arguments.
+int check_recurrence(const gated_recurrence_args *args, const char *op, bool step) {
+    if (!args) return set_error(CONV2D_EINVAL, "%s: args must not be null", op);
+    const gated_recurrence_args &a = *args;
+    Shape s{op, a.tokens, a.nseq, a.dtype, false, step};
+    int rc = check_shape(&s, a.offsets, a.slots, a.state_rows);
+    if (rc) return rc;
+    if (a.channels <= 0) return set_error(CONV2D_EINVAL, "%s: channels must be positive (got %d)", op, a.channels);
+    if (a.channels > kMaxWidth) return too_wide(op);
+    if (a.longest < 0) return set_error(CONV2D_EINVAL, "%s: longest must not be negative", op);
+    if (!aligned_floats({a.forget_bias}))
+        return set_error(CONV2D_EINVAL, "%s: forget_bias is not aligned to its type", op);
+    if (s.nseq == 0) return CONV2D_OK;
+    const Rows rows[] = {{"x", a.x, a.x_batch, a.x_token, a.channels},
+                         {"forget", a.forget, a.forget_batch, a.forget_token, a.channels},
+                         {"y", a.y, a.y_batch, a.y_token, a.channels},
+                         {"gate", a.gate, a.gate_batch, a.gate_token, a.channels}};
+    Extent in[4];
+    for (int i = 0; i < 4; i++) {
+        const long long n = i == 3 && !a.gate ? 0 : rows_bytes(s, rows[i]);
+        if (n < 0) return (int)n;
+        in[i] = Extent{rows[i].name, rows[i].p, n};
+    }
+    if (!rows_disjoint(s, rows[2])) return set_error(CONV2D_EINVAL, "%s: rows of y overlap each other", op);
+    const long long sb = state_bytes(op, a.state, a.state_rows, a.channels, 4);
+    if (sb < 0) return (int)sb;
+    const Extent es{"state", a.state, sb}, eb{"forget_bias", a.forget_bias, 4ll * a.channels};
+    const Extent eo{"offsets", a.offsets, 4ll * (a.nseq + 1ll)}, el{"slots", a.slots, 4ll * a.nseq};
+    rc = check_no_overlap(op, in[2], {in[0], in[1], in[3], es, eb, eo, el});
+    if (!rc) rc = check_no_overlap(op, es, {in[0], in[1], in[3], eb, eo, el});
+    return rc;
+}
+
+// Whether the rows of two outputs share a value: neither apart as wholes nor column slices of
+// the same wider rows.
+bool rows_share(const Shape &s, const Rows &a, long long abytes, const Rows &b, long long bbytes) {
+    if (!overlap(a.p, abytes, b.p, bbytes)) return false;
+    if (a.token != b.token || (!s.step && !s.packed && a.batch != b.batch)) return true;
+    const Rows &lo = (uintptr_t)a.p <= (uintptr_t)b.p ? a : b, &hi = &lo == &a ? b : a;
+    const long long apart = (long long)((uintptr_t)hi.p - (uintptr_t)lo.p) / dtype_bytes(s.dtype);
+    return apart < lo.width || !rows_disjoint(s, Rows{lo.name, lo.p, lo.batch, lo.token, apart + hi.width});
+}
+
+int check_recurrence_backward(const gated_recurrence_backward_args *args, const char *op) {
+    if (!args) return set_error(CONV2D_EINVAL, "%s: args must not be null", op);
+    const gated_recurrence_backward_args &a = *args;
+    Shape s{op, a.tokens, a.nseq, a.dtype, false, false};
+    int rc = check_shape(&s, a.offsets, a.slots, a.state_rows);
+    if (rc) return rc;
+    if (a.channels <= 0) return set_error(CONV2D_EINVAL, "%s: channels must be positive (got %d)", op, a.channels);
+    if (a.channels > kMaxWidth) return too_wide(op);
+    if (a.longest < 0) return set_error(CONV2D_EINVAL, "%s: longest must not be negative", op);
+    if (!aligned_floats({a.forget_bias, a.grad_forget_bias}))
+        return set_error(CONV2D_EINVAL, "%s: forget_bias or grad_forget_bias is not aligned to its type", op);
+    if (!a.gate != !a.grad_gate)
+        return set_error(CONV2D_EINVAL, "%s: gate and grad_gate must both be given or neither", op);
+    if (s.nseq == 0) return CONV2D_OK;
+    const Rows rows[] = {{"grad", a.grad, a.grad_batch, a.grad_token, a.channels},
+                         {"x", a.x, a.x_batch, a.x_token, a.channels},
+                         {"forget", a.forget, a.forget_batch, a.forget_token, a.channels},
+                         {"gate", a.gate, a.gate_batch, a.gate_token, a.channels},
+                         {"grad_x", a.grad_x, a.grad_x_batch, a.grad_x_token, a.channels},
+                         {"grad_forget", a.grad_forget, a.grad_forget_batch, a.grad_forget_token, a.channels},
+                         {"grad_gate", a.grad_gate, a.grad_gate_batch, a.grad_gate_token, a.channels}};
+    Extent e[7];
+    for (int i = 0; i < 7; i++) {
+        const long long n = !a.gate && (i == 3 || i == 6) ? 0 : rows_bytes(s, rows[i]);
+        if (n < 0) return (int)n;
+        e[i] = Extent{rows[i].name, rows[i].p, n};
+    }
+    const long long sb = state_bytes(op, a.state, a.state_rows, a.channels, 4);
+    const long long gb = state_bytes(op, a.grad_state, a.state_rows, a.channels, 4);
+    if (sb < 0 || gb < 0) return (int)(sb < 0 ? sb : gb);
+    const Extent es{"state", a.state, sb}, eg{"grad_state", a.grad_state, gb};
+    const Extent eb{"forget_bias", a.forget_bias, 4ll * a.channels};
+    const Extent ed{"grad_forget_bias", a.grad_forget_bias, 4ll * a.channels};
+    const Extent eo{"offsets", a.offsets, 4ll * (a.nseq + 1ll)}, el{"slots", a.slots, 4ll * a.nseq};
+    for (int i = 4; i < 7; i++) {
+        if (!e[i].bytes) continue;
+        if (!rows_disjoint(s, rows[i]))
+            return set_error(CONV2D_EINVAL, "%s: rows of %s overlap each other", op, rows[i].name);
+        for (int j = 4; j < i; j++)
+            if (e[j].bytes && rows_share(s, rows[j], e[j].bytes, rows[i], e[i].bytes))
+                return set_error(CONV2D_EINVAL, "%s: %s overlaps %s", op, rows[i].name, rows[j].name);
+        rc = check_no_overlap(op, e[i], {e[0], e[1], e[2], e[3], es, eg, eb, ed, eo, el});
+        if (rc) return rc;
+    }
+    rc = check_no_overlap(op, eg, {e[0], e[1], e[2], e[3], es, eb, ed, eo, el});
+    if (!rc) rc = check_no_overlap(op, ed, {e[0], e[1], e[2], e[3], es, eb, eo, el});
+    return rc;
+}
+
 int check_w4(const char *op, int out_features, int in_features, int group) {
     if (out_features <= 0 || in_features <= 0)
         return set_error(CONV2D_EINVAL, "%s: sizes must be positive (out %d, in %d)", op, out_features, in_features);
@@ -234,6 +326,52 @@ int selective_scan_workspace_size(const selective_scan_args *args, size_t *bytes
 }
 
 int selective_scan_step(const selective_scan_args *args, void *stream) { return run_scan(args, true, stream); }
+
+int gated_recurrence(const gated_recurrence_args *args, void *stream) {
+    const char *op = "gated_recurrence";
+    const int rc = check_recurrence(args, op, false);
+    if (rc) return rc;
+    if (args->nseq == 0) return set_ok();
+    const Workspace ws = current_ws();
+    return launched(op, launch_recurrence(*args, ws.p, ws.bytes, static_cast<hipStream_t>(stream)));
+}
+
+int gated_recurrence_workspace_size(const gated_recurrence_args *args, size_t *bytes) {
+    const char *op = "gated_recurrence_workspace_size";
+    if (!bytes) return set_error(CONV2D_EINVAL, "%s: bytes must not be null", op);
+    const int rc = check_recurrence(args, op, false);
+    if (rc) return rc;
+    *bytes = args->nseq ? recurrence_workspace(*args) : 0;
+    return set_ok();
+}
+
+int gated_recurrence_step(const gated_recurrence_args *args, void *stream) {
+    const char *op = "gated_recurrence_step";
+    const int rc = check_recurrence(args, op, true);
+    if (rc) return rc;
+    if (args->nseq == 0) return set_ok();
+    return launched(op, launch_recurrence_token(*args, static_cast<hipStream_t>(stream)));
+}
+
+int gated_recurrence_backward(const gated_recurrence_backward_args *args, void *stream) {
+    const char *op = "gated_recurrence_backward";
+    const int rc = check_recurrence_backward(args, op);
+    if (rc) return rc;
+    const Workspace ws = current_ws();
+    const size_t need = recurrence_backward_workspace(*args);
+    if (need > (ws.p ? ws.bytes : 0))
+        return set_error(CONV2D_EUNSUPPORTED, "%s: needs a workspace of %zu bytes (set: %zu)", op, need, ws.p ? ws.bytes : 0);
+    return launched(op, launch_recurrence_backward(*args, ws.p, static_cast<hipStream_t>(stream)));
+}
+
+int gated_recurrence_backward_workspace_size(const gated_recurrence_backward_args *args, size_t *bytes) {
+    const char *op = "gated_recurrence_backward_workspace_size";
+    if (!bytes) return set_error(CONV2D_EINVAL, "%s: bytes must not be null", op);
+    const int rc = check_recurrence_backward(args, op);
+    if (rc) return rc;
+    *bytes = recurrence_backward_workspace(*args);
+    return set_ok();
+}
 
 int matvec_w4_packed_bytes(int out_features, int in_features, int group, int has_zeros, size_t *bytes) {
     const char *op = "matvec_w4_packed_bytes";

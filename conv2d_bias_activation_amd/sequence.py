@@ -22,12 +22,14 @@ import torch
 
 from . import _ACTS, _DTYPES, RES_BEFORE_ACT, _check, _load, _use_workspace, _ws_cache, _ws_key
 
-__all__ = ["causal_conv1d", "causal_conv1d_step", "selective_scan", "selective_scan_step", "w4_pack", "matvec_w4",
-           "W4Weights"]
+__all__ = ["causal_conv1d", "causal_conv1d_step", "selective_scan", "selective_scan_step", "gated_recurrence",
+           "gated_recurrence_step", "gated_recurrence_backward", "w4_pack", "matvec_w4", "W4Weights"]
 
-# struct causal_conv1d_args, selective_scan_args and matvec_w4_args, field by field
+# the argument structs of include/sequence_ops.h, field by field
 _CONV = struct.Struct("@8P5q7i0q")
 _SCAN = struct.Struct("@12P14q8i0q")
+_REC = struct.Struct("@8P10q6i0q")
+_REC_BACK = struct.Struct("@13P16q5i0q")
 _W4 = struct.Struct("@6P3q7i0q")
 
 
@@ -272,6 +274,119 @@ def selective_scan_step(u, dt, A, B, C, *, state, skip=None, gate=None, dt_bias=
     """selective_scan for one token of each sequence: u [sequences, channels], B [sequences, groups, states]."""
     return _scan("selective_scan_step", u, dt, A, B, C, skip, gate, dt_bias, softplus, state, slots, False, None, None,
                  out, stream, False, True)
+
+
+def _strides(t, batched):
+    """(batch stride, token stride) of token rows or None."""
+    return (0, 0) if t is None else t.stride()[:2] if batched else (0, t.stride(0))
+
+
+def _recurrence(name, x, forget, gate, forget_bias, coupled, state, slots, fresh, seq_offsets, longest, out, stream, workspace,
+                step):
+    dt = _storage(x)
+    dev, dtype, shape = x.device, x.dtype, x.shape
+    nseq, tokens, *x_strides = _geometry(x, seq_offsets, step)
+    channels = shape[-1]
+    xp = _rows("x", x, shape, dtype, dev)
+    fp = _rows("forget", forget, shape, dtype, dev)
+    gp = 0 if gate is None else _rows("gate", gate, shape, dtype, dev)
+    bp = _dense("forget_bias", forget_bias, (channels,), torch.float32, dev)
+    sp, rows = _state_rows(state, (channels,), torch.float32, dev)
+    op = _dense("seq_offsets", seq_offsets, (nseq + 1,), torch.int32, dev)
+    lp = _dense("slots", slots, (nseq,), torch.int32, dev)
+    if out is None:
+        out = _new_like(x, stream)
+        yp = out.data_ptr()
+    else:
+        yp = _rows("out", out, shape, dtype, dev)
+    batched = len(shape) == 3
+    args = _REC.pack(xp, fp, gp, bp, sp, yp, op, lp, *x_strides, *_strides(forget, batched), *_strides(gate, batched),
+                     *_strides(out, batched), tokens, longest or 0, nseq, rows, channels, 1 if coupled else 0, dt,
+                     1 if fresh else 0)
+    if not step:
+        need = 0
+        if workspace is None:
+            size = ctypes.c_size_t(0)
+            _check(_load().gated_recurrence_workspace_size(args, ctypes.byref(size)))
+            need = size.value
+        if need or workspace is not None:
+            _scratch(dev, stream, workspace, need)
+    _call(name, args, dev, stream)
+    return out
+
+
+def gated_recurrence(x, forget, *, gate=None, forget_bias=None, coupled=True, state=None, slots=None, fresh=False,
+                     seq_offsets=None, longest=None, out=None, stream=None, workspace=None):
+    """Gated linear recurrence along each sequence. With f = sigmoid(forget[t, c] + forget_bias[c])
+    and h the [channels] state:
+
+        h[c] = f * h[c] + (1 - f) * x[t, c]        (coupled=False: f * h[c] + x[t, c])
+        y[t, c] = h[c] * silu(gate[t, c])          (without a gate: h[c])
+
+    x, forget, gate: [batch, tokens, channels], or packed [tokens, channels] with ``seq_offsets``
+    (int32 [sequences + 1] on the GPU), of one dtype (float32, bfloat16 or float16), any strides
+    but the last. forget_bias: float32 [channels]. ``state`` float32 [rows, channels] is read and
+    updated in place; ``slots``, ``fresh``, ``longest`` and ``workspace`` as for selective_scan.
+    Returns y, shaped as x."""
+    return _recurrence("gated_recurrence", x, forget, gate, forget_bias, coupled, state, slots, fresh, seq_offsets, longest,
+                       out, stream, workspace, False)
+
+
+def gated_recurrence_step(x, forget, *, state, gate=None, forget_bias=None, coupled=True, slots=None, out=None, stream=None):
+    """gated_recurrence for one token of each sequence: x [sequences, channels]."""
+    return _recurrence("gated_recurrence_step", x, forget, gate, forget_bias, coupled, state, slots, False, None, None, out,
+                       stream, False, True)
+
+
+def gated_recurrence_backward(grad, x, forget, *, gate=None, forget_bias=None, coupled=True, state=None, grad_state=None,
+                              slots=None, seq_offsets=None, longest=None, out=None, stream=None, workspace=None):
+    """Gradient of gated_recurrence, from ``grad``, that of y: (grad_x, grad_forget, grad_gate,
+    grad_forget_bias), None in the place of an input that is None.
+
+    The other inputs are those of the forward call; ``state`` is a copy of the states from before
+    it (None: the sequences started from zeros, as with ``fresh``) and is only read. ``grad_state``
+    float32 [rows, channels] is updated in place, from the gradient of the state that a sequence
+    left to that of the state it started from (None: the states left are of no further use).
+    ``out``: tensors (grad_x, grad_forget, grad_gate or None) to write, which may be column slices
+    of one tensor; grad_forget_bias is float32 and always new. Needs a workspace, so no
+    ``workspace=False``."""
+    dt = _storage(x)
+    dev, dtype, shape = x.device, x.dtype, x.shape
+    nseq, tokens, *x_strides = _geometry(x, seq_offsets, False)
+    channels = shape[-1]
+    xp = _rows("x", x, shape, dtype, dev)
+    ep = _rows("grad", grad, shape, dtype, dev)
+    fp = _rows("forget", forget, shape, dtype, dev)
+    gp = 0 if gate is None else _rows("gate", gate, shape, dtype, dev)
+    bp = _dense("forget_bias", forget_bias, (channels,), torch.float32, dev)
+    sp, rows = _state_rows(state, (channels,), torch.float32, dev)
+    hp, grad_rows = _state_rows(grad_state, (channels,), torch.float32, dev)
+    if state is not None and grad_state is not None and rows != grad_rows:
+        _fail("grad_state", f"must have shape {tuple(state.shape)}, has {tuple(grad_state.shape)}")
+    op = _dense("seq_offsets", seq_offsets, (nseq + 1,), torch.int32, dev)
+    lp = _dense("slots", slots, (nseq,), torch.int32, dev)
+    if out is None:
+        gx, gf, gg = _new_like(x, stream), _new_like(x, stream), None if gate is None else _new_like(x, stream)
+    else:
+        gx, gf, gg = out
+        if (gg is None) != (gate is None):
+            _fail("out", "must have grad_gate where there is a gate, and only there")
+    outs = (_rows("grad_x", gx, shape, dtype, dev), _rows("grad_forget", gf, shape, dtype, dev),
+            0 if gg is None else _rows("grad_gate", gg, shape, dtype, dev))
+    gb = None if forget_bias is None else _new((channels,), torch.float32, dev, stream)
+    batched = len(shape) == 3
+    args = _REC_BACK.pack(ep, xp, fp, gp, bp, sp, hp, *outs, 0 if gb is None else gb.data_ptr(), op, lp,
+                          *_strides(grad, batched), *x_strides, *_strides(forget, batched), *_strides(gate, batched),
+                          *_strides(gx, batched), *_strides(gf, batched), *_strides(gg, batched), tokens, longest or 0, nseq,
+                          max(rows, grad_rows), channels, 1 if coupled else 0, dt)
+    need = 0
+    if workspace is None:
+        size = ctypes.c_size_t(0)
+        _check(_load().gated_recurrence_backward_workspace_size(args, ctypes.byref(size)))
+        need = size.value
+    _scratch(dev, stream, workspace, need)
+    _call("gated_recurrence_backward", args, dev, stream)
+    return gx, gf, gg, gb
 
 
 class W4Weights:

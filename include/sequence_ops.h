@@ -1,7 +1,8 @@
 /*
  * sequence_ops.h - C ABI of the sequence operators of libconv2d_fused for MI355X (gfx950):
- * the short causal convolution and the selective state space scan, for prompts and for
- * single tokens, and products of a few token rows with 4-bit weights.
+ * the short causal convolution, the selective state space scan and the gated linear
+ * recurrence, for prompts and for single tokens, the recurrence's gradient, products of a few
+ * token rows with 4-bit weights, and products of any number of them in 8-bit integers.
  *
  * The conventions of conv2d_fused.h hold (device pointers owned by the caller, work only
  * enqueued on `stream`, arguments validated on the host before anything is launched, status
@@ -113,6 +114,77 @@ int selective_scan_workspace_size(const selective_scan_args *args, size_t *bytes
 
 /* The same for one token of each of nseq sequences, as causal_conv1d_step. */
 int selective_scan_step(const selective_scan_args *args, void *stream);
+
+/* With f = 1 / (1 + exp(-(forget[t, c] + forget_bias[c]))) and h the state of the sequence:
+ *     h[c] = f * h[c] + (1 - f) * x[t, c]                (coupled), or f * h[c] + x[t, c]
+ *     y[t, c] = h[c] * gate[t, c] / (1 + exp(-gate[t, c])), or h[c] without a gate
+ * The state and every intermediate are fp32; y is rounded once. An infinity or NaN in an input
+ * may make y, and through the state the later y, infinite or NaN in the channels and the
+ * sequence that read it, and in no others. */
+typedef struct gated_recurrence_args {
+    const void *x, *forget; /* token rows of `channels` values */
+    const void *gate;       /* token rows of `channels` values, or NULL */
+    const float *forget_bias; /* [channels] or NULL */
+    float *state;           /* [state_rows, channels], contiguous, or NULL */
+    void *y;                /* token rows of `channels` values */
+    const int *offsets;     /* see above */
+    const int *slots;       /* see above */
+    long long x_batch, x_token, forget_batch, forget_token, gate_batch, gate_token, y_batch, y_token; /* in elements */
+    long long tokens;
+    long long longest;      /* as for selective_scan */
+    int nseq, state_rows, channels;
+    int coupled;
+    int dtype;              /* of x, forget, gate and y */
+    int fresh;
+} gated_recurrence_args;
+
+/* Long sequences are cut into chunks that run side by side where the calling thread's
+ * workspace holds gated_recurrence_workspace_size() bytes (0: the call is not split). Without
+ * it the call gives the same results up to rounding, slower. The size is host only. */
+int gated_recurrence(const gated_recurrence_args *args, void *stream);
+int gated_recurrence_workspace_size(const gated_recurrence_args *args, size_t *bytes);
+
+/* The same for one token of each of nseq sequences, as causal_conv1d_step. */
+int gated_recurrence_step(const gated_recurrence_args *args, void *stream);
+
+/* The gradient of gated_recurrence. Given grad, the gradient of a loss with respect to y, it
+ * writes those with respect to x, forget, gate (with a gate) and forget_bias (unless
+ * grad_forget_bias is NULL). With g_t the gradient with respect to h_t, which is grad times
+ * silu(gate) plus f_{t+1} g_{t+1}:
+ *     grad_x = g (1 - f) or g,    grad_forget = g (h_{t-1} - x or h_{t-1}) f (1 - f),
+ *     grad_gate = grad h_t silu'(gate),    grad_forget_bias = sum of grad_forget over all tokens
+ * States: `state` holds the rows that the sequences started from (NULL, or a slot outside it:
+ * zeros) and is only read; the forward call has updated its own in place, so the caller keeps a
+ * copy. grad_state, [state_rows, channels], holds for each sequence the gradient with respect to
+ * the state that it left (NULL: zero) and afterwards that with respect to the state, or the
+ * zeros, that it started from.
+ * Everything is fp32 but the values read and, rounded once each, grad_x, grad_forget and
+ * grad_gate. The sum over tokens has a fixed order. The outputs may be column slices of one
+ * tensor with the same strides (rows that interleave without sharing a value); they may overlap
+ * no input. Needs gated_recurrence_backward_workspace_size() bytes of workspace, and returns
+ * CONV2D_EUNSUPPORTED where the thread's is smaller. */
+typedef struct gated_recurrence_backward_args {
+    const void *grad, *x, *forget; /* token rows of `channels` values */
+    const void *gate;       /* token rows of `channels` values, or NULL */
+    const float *forget_bias; /* [channels] or NULL */
+    const float *state;     /* [state_rows, channels], contiguous, or NULL */
+    float *grad_state;      /* [state_rows, channels], contiguous, or NULL */
+    void *grad_x, *grad_forget; /* token rows of `channels` values */
+    void *grad_gate;        /* token rows of `channels` values; NULL without a gate */
+    float *grad_forget_bias; /* [channels] or NULL */
+    const int *offsets;     /* see above */
+    const int *slots;       /* see above */
+    long long grad_batch, grad_token, x_batch, x_token, forget_batch, forget_token, gate_batch, gate_token; /* in elements */
+    long long grad_x_batch, grad_x_token, grad_forget_batch, grad_forget_token, grad_gate_batch, grad_gate_token;
+    long long tokens;
+    long long longest;      /* as for selective_scan */
+    int nseq, state_rows, channels;
+    int coupled;
+    int dtype;              /* of the token rows */
+} gated_recurrence_backward_args;
+
+int gated_recurrence_backward(const gated_recurrence_backward_args *args, void *stream);
+int gated_recurrence_backward_workspace_size(const gated_recurrence_backward_args *args, size_t *bytes);
 
 /* 4-bit weights: weight (o, k) is (code - zero) * scale with a code of 0 .. 15 and, for each
  * run of `group` inputs (32, 64 or 128; the last one may be shorter) of an output, a scale
