@@ -35,7 +35,7 @@ __all__ = ["conv2d_fused", "conv2d_fused_maxpool3x3s2", "maxpool3x3s2", "avgpool
            "ACT_PRELU", "RES_BEFORE_ACT", "LAYOUT_NHWC", "LAYOUT_NCHW", "DTYPE_F32",
            "DTYPE_BF16", "DTYPE_F16", "causal_conv1d", "causal_conv1d_step", "selective_scan",
            "selective_scan_step", "gated_recurrence", "gated_recurrence_step", "gated_recurrence_backward",
-           "w4_pack", "matvec_w4", "W4Weights"]
+           "w4_pack", "matvec_w4", "W4Weights", "quantize_rows", "q8_pack", "q8_unpack", "matmul_q8", "Q8Rows"]
 
 # Codes of include/conv2d_fused.h
 LAYOUT_NHWC, LAYOUT_NCHW = 0, 1
@@ -120,6 +120,12 @@ SEQUENCE_SIGNATURES = {
     "matvec_w4_packed_bytes": (_i, [_i] * 4 + [ctypes.POINTER(ctypes.c_size_t)]),
     "matvec_w4_pack": (_i, [_vp] * 4 + [_i] * 4 + [_vp]),
     "matvec_w4": (_i, [_cp, _vp]),
+    "q8_packed_bytes": (_i, [_i, _i, ctypes.POINTER(ctypes.c_size_t)]),
+    "quantize_rows": (_i, [_cp, _vp]),
+    "q8_pack": (_i, [_vp, _vp, _vp, _i, _i, _vp]),
+    "q8_unpack": (_i, [_vp, _vp, _vp, _i, _i, _vp]),
+    "matmul_q8": (_i, [_cp, _vp]),
+    "matmul_q8_workspace_size": (_i, [_cp, ctypes.POINTER(ctypes.c_size_t)]),
 }
 
 _lib = None
@@ -802,6 +808,6 @@ def weights_to_ohwi(w, stream=None):
     return w2
 
 
-from .sequence import (W4Weights, causal_conv1d, causal_conv1d_step, gated_recurrence,  # noqa: E402
-                       gated_recurrence_backward, gated_recurrence_step, matvec_w4, selective_scan,
-                       selective_scan_step, w4_pack)
+from .sequence import (Q8Rows, W4Weights, causal_conv1d, causal_conv1d_step, gated_recurrence,  # noqa: E402
+                       gated_recurrence_backward, gated_recurrence_step, matmul_q8, matvec_w4, q8_pack, q8_unpack,
+                       quantize_rows, selective_scan, selective_scan_step, w4_pack)

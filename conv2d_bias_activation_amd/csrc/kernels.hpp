@@ -243,5 +243,10 @@ size_t w4_packed_bytes(int out_features, int in_features, int group, bool zeros)
 hipError_t launch_w4_pack(const void *codes, const void *scales, const void *zeros, void *packed, int out_features,
                           int in_features, int group, int dtype, hipStream_t st);
 hipError_t launch_matvec_w4(const matvec_w4_args &a, hipStream_t st);
+size_t q8_bytes(int rows, int in_features);
+hipError_t launch_quantize_rows(const quantize_rows_args &a, hipStream_t st);
+hipError_t launch_q8_pack(const void *codes, const float *scales, void *packed, int rows, int in_features, hipStream_t st);
+hipError_t launch_q8_unpack(const void *packed, void *codes, float *scales, int rows, int in_features, hipStream_t st);
+hipError_t launch_matmul_q8(const matmul_q8_args &a, void *ws, hipStream_t st);  // ws: q8_bytes for x
 
 }  // namespace c2d

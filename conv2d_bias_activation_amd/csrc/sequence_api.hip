@@ -306,6 +306,68 @@ int check_w4(const char *op, int out_features, int in_features, int group) {
     return CONV2D_OK;
 }
 
+constexpr int kMaxInputs = (1 << 17) - 1;  // sums of 2^17 products of -128 would pass 2^31
+
+int check_q8(const char *op, int rows, int in_features) {
+    if (rows < 0 || in_features <= 0)
+        return set_error(CONV2D_EINVAL, "%s: rows must not be negative and in_features positive (got %d and %d)", op, rows,
+                         in_features);
+    if (in_features > kMaxInputs)
+        return set_error(CONV2D_EUNSUPPORTED, "%s: more than 2^17 - 1 inputs are not supported (got %d)", op, in_features);
+    if (rows > kMaxWidth || (long long)rows * in_features > 1ll << 40)
+        return set_error(CONV2D_EUNSUPPORTED, "%s: more than 2^30 rows or 2^40 values are not supported", op);
+    return CONV2D_OK;
+}
+
+int check_quantize(const quantize_rows_args *args, const char *op) {
+    if (!args) return set_error(CONV2D_EINVAL, "%s: args must not be null", op);
+    const quantize_rows_args &a = *args;
+    int rc = check_q8(op, a.rows, a.in_features);
+    if (rc) return rc;
+    Shape s{op, 1, a.rows, a.dtype, false, true};
+    rc = check_shape(&s, nullptr, nullptr, 0);
+    if (rc || a.rows == 0) return rc;
+    if (!a.packed || !aligned16(a.packed))
+        return set_error(CONV2D_EINVAL, "%s: packed must not be null and 16-byte aligned", op);
+    const long long xb = rows_bytes(s, Rows{"x", a.x, 0, a.x_row, a.in_features});
+    if (xb < 0) return (int)xb;
+    return check_no_overlap(op, Extent{"packed", a.packed, (long long)q8_bytes(a.rows, a.in_features)}, {Extent{"x", a.x, xb}});
+}
+
+int check_matmul_q8(const matmul_q8_args *args, const char *op) {
+    if (!args) return set_error(CONV2D_EINVAL, "%s: args must not be null", op);
+    const matmul_q8_args &a = *args;
+    int rc = check_q8(op, a.rows, a.in_features);
+    if (!rc && a.out_features <= 0)
+        rc = set_error(CONV2D_EINVAL, "%s: out_features must be positive (got %d)", op, a.out_features);
+    if (!rc) rc = check_q8(op, a.out_features, a.in_features);
+    if (!rc) rc = check_act(op, a.act, a.alpha, CONV2D_RES_BEFORE_ACT);
+    if (rc) return rc;
+    Shape s{op, 1, a.rows, a.dtype, false, true};
+    rc = check_shape(&s, nullptr, nullptr, 0);
+    if (rc) return rc;
+    if (!a.weights || !aligned16(a.weights))
+        return set_error(CONV2D_EINVAL, "%s: weights must not be null and 16-byte aligned", op);
+    if (!aligned_floats({a.bias, a.alpha}))
+        return set_error(CONV2D_EINVAL, "%s: bias or alpha is not aligned to its type", op);
+    if (a.rows == 0) return CONV2D_OK;
+    if (!a.x == !a.x_packed || !aligned16(a.x_packed))
+        return set_error(CONV2D_EINVAL, "%s: takes either x or x_packed, the latter 16-byte aligned", op);
+    const Rows x{"x", a.x, 0, a.x_row, a.in_features}, y{"y", a.y, 0, a.y_row, a.out_features};
+    const Rows r{"residual", a.residual, 0, a.residual_row, a.out_features};
+    const long long xb = a.x ? rows_bytes(s, x) : 0, yb = rows_bytes(s, y), rb = a.residual ? rows_bytes(s, r) : 0;
+    if (xb < 0 || yb < 0 || rb < 0) return (int)(xb < 0 ? xb : yb < 0 ? yb : rb);
+    if (!rows_disjoint(s, y)) return set_error(CONV2D_EINVAL, "%s: rows of y overlap each other", op);
+    return check_no_overlap(
+        op, Extent{"y", a.y, yb},
+        {Extent{"x", a.x, xb}, Extent{"x_packed", a.x_packed, (long long)q8_bytes(a.rows, a.in_features)},
+         Extent{"weights", a.weights, (long long)q8_bytes(a.out_features, a.in_features)}, Extent{"residual", a.residual, rb},
+         Extent{"bias", a.bias, 4ll * a.out_features},
+         Extent{"alpha", (a.act & 0xff) == CONV2D_ACT_PRELU ? a.alpha : nullptr, 4ll * a.out_features}});
+}
+
+size_t q8_need(const matmul_q8_args &a) { return a.rows && a.x ? q8_bytes(a.rows, a.in_features) : 0; }
+
 bool type16(int dtype) { return dtype == CONV2D_DTYPE_BF16 || dtype == CONV2D_DTYPE_F16; }
 
 }  // namespace
@@ -429,6 +491,73 @@ int matvec_w4(const matvec_w4_args *args, void *stream) {
                            Extent{"alpha", (a.act & 0xff) == CONV2D_ACT_PRELU ? a.alpha : nullptr, 4ll * a.out_features}});
     if (rc) return rc;
     return launched(op, launch_matvec_w4(a, static_cast<hipStream_t>(stream)));
+}
+
+int q8_packed_bytes(int rows, int in_features, size_t *bytes) {
+    const char *op = "q8_packed_bytes";
+    if (!bytes) return set_error(CONV2D_EINVAL, "%s: bytes must not be null", op);
+    const int rc = check_q8(op, rows, in_features);
+    if (rc) return rc;
+    *bytes = q8_bytes(rows, in_features);
+    return set_ok();
+}
+
+int quantize_rows(const quantize_rows_args *args, void *stream) {
+    const char *op = "quantize_rows";
+    const int rc = check_quantize(args, op);
+    if (rc) return rc;
+    if (args->rows == 0) return set_ok();
+    return launched(op, launch_quantize_rows(*args, static_cast<hipStream_t>(stream)));
+}
+
+int q8_pack(const void *codes, const float *scales, void *packed, int rows, int in_features, void *stream) {
+    const char *op = "q8_pack";
+    const int rc = check_q8(op, rows, in_features);
+    if (rc) return rc;
+    if (rows == 0) return set_ok();
+    if (!codes || !scales || !packed) return set_error(CONV2D_EINVAL, "%s: codes, scales and packed must not be null", op);
+    if (!aligned16(packed) || (uintptr_t)scales % 4)
+        return set_error(CONV2D_EINVAL, "%s: packed must be 16-byte and scales 4-byte aligned", op);
+    const long long bytes = (long long)q8_bytes(rows, in_features);
+    if (overlap(packed, bytes, codes, (long long)rows * in_features) || overlap(packed, bytes, scales, 4ll * rows))
+        return set_error(CONV2D_EINVAL, "%s: packed overlaps an input", op);
+    return launched(op, launch_q8_pack(codes, scales, packed, rows, in_features, static_cast<hipStream_t>(stream)));
+}
+
+int q8_unpack(const void *packed, void *codes, float *scales, int rows, int in_features, void *stream) {
+    const char *op = "q8_unpack";
+    const int rc = check_q8(op, rows, in_features);
+    if (rc) return rc;
+    if (rows == 0) return set_ok();
+    if (!codes || !scales || !packed) return set_error(CONV2D_EINVAL, "%s: codes, scales and packed must not be null", op);
+    if (!aligned16(packed) || (uintptr_t)scales % 4)
+        return set_error(CONV2D_EINVAL, "%s: packed must be 16-byte and scales 4-byte aligned", op);
+    const long long bytes = (long long)q8_bytes(rows, in_features), n = (long long)rows * in_features;
+    if (overlap(packed, bytes, codes, n) || overlap(packed, bytes, scales, 4ll * rows) || overlap(codes, n, scales, 4ll * rows))
+        return set_error(CONV2D_EINVAL, "%s: an output overlaps another operand", op);
+    return launched(op, launch_q8_unpack(packed, codes, scales, rows, in_features, static_cast<hipStream_t>(stream)));
+}
+
+int matmul_q8(const matmul_q8_args *args, void *stream) {
+    const char *op = "matmul_q8";
+    const int rc = check_matmul_q8(args, op);
+    if (rc) return rc;
+    if (args->rows == 0) return set_ok();
+    const Workspace ws = current_ws();
+    const size_t need = q8_need(*args);
+    if (need > (ws.p ? ws.bytes : 0))
+        return set_error(CONV2D_EUNSUPPORTED, "%s: needs a workspace of %zu bytes (set: %zu), or rows from quantize_rows", op, need,
+                         ws.p ? ws.bytes : 0);
+    return launched(op, launch_matmul_q8(*args, ws.p, static_cast<hipStream_t>(stream)));
+}
+
+int matmul_q8_workspace_size(const matmul_q8_args *args, size_t *bytes) {
+    const char *op = "matmul_q8_workspace_size";
+    if (!bytes) return set_error(CONV2D_EINVAL, "%s: bytes must not be null", op);
+    const int rc = check_matmul_q8(args, op);
+    if (rc) return rc;
+    *bytes = q8_need(*args);
+    return set_ok();
 }
 
 }  // extern "C"

@@ -23,7 +23,8 @@ import torch
 from . import _ACTS, _DTYPES, RES_BEFORE_ACT, _check, _load, _use_workspace, _ws_cache, _ws_key
 
 __all__ = ["causal_conv1d", "causal_conv1d_step", "selective_scan", "selective_scan_step", "gated_recurrence",
-           "gated_recurrence_step", "gated_recurrence_backward", "w4_pack", "matvec_w4", "W4Weights"]
+           "gated_recurrence_step", "gated_recurrence_backward", "w4_pack", "matvec_w4", "W4Weights",
+           "quantize_rows", "q8_pack", "q8_unpack", "matmul_q8", "Q8Rows"]
 
 # the argument structs of include/sequence_ops.h, field by field
 _CONV = struct.Struct("@8P5q7i0q")
@@ -31,6 +32,8 @@ _SCAN = struct.Struct("@12P14q8i0q")
 _REC = struct.Struct("@8P10q6i0q")
 _REC_BACK = struct.Struct("@13P16q5i0q")
 _W4 = struct.Struct("@6P3q7i0q")
+_QUANTIZE = struct.Struct("@2P1q3i0q")
+_Q8 = struct.Struct("@7P3q5i0q")
 
 
 def _stream_handle(index):
@@ -451,4 +454,105 @@ def matvec_w4(x, weights, bias=None, alpha=None, residual=None, *, act="none", r
                                 0 if residual is None else residual.stride(0), out.stride(0), rows,
                                 weights.in_features, n, weights.group, 1 if weights.zeros else 0,
                                 _act(act) | (RES_BEFORE_ACT if res_before_act else 0), dt), dev, stream)
+    return out
+
+
+class Q8Rows:
+    """Rows in 8 bits with a scale each, laid out by quantize_rows or q8_pack for matmul_q8 (``data``:
+    the packed bytes; ``dtype``: that of the values, and of a product's output)."""
+    __slots__ = ("data", "rows", "in_features", "dtype", "device")
+
+    def __init__(self, data, rows, in_features, dtype):
+        self.data, self.rows, self.in_features, self.dtype, self.device = data, rows, in_features, dtype, data.device
+
+
+def _q8_new(rows, k, device, stream):
+    nbytes = ctypes.c_size_t(0)
+    _check(_load().q8_packed_bytes(rows, k, ctypes.byref(nbytes)))
+    return _new((nbytes.value,), torch.uint8, device, stream)
+
+
+def quantize_rows(x, *, stream=None):
+    """Rows x [rows, in_features] (float32, bfloat16 or float16, rows at any stride) in 8 bits: for
+    each row the scale max(|x|) / 127, in float32 and at least 2^-126, and the codes x / scale,
+    rounded to the nearest whole number, ties to even. A row with an infinity or a NaN gets a
+    scale of NaN. Returns Q8Rows, for products of these tokens with several weights, or weights."""
+    dt = _storage(x)
+    if x.dim() != 2:
+        _fail("x", "must be [rows, in_features]")
+    rows, k = x.shape
+    xp = _rows("x", x, x.shape, x.dtype, x.device)
+    data = _q8_new(rows, k, x.device, stream)
+    _call("quantize_rows", _QUANTIZE.pack(xp, data.data_ptr(), x.stride(0), rows, k, dt), x.device, stream)
+    return Q8Rows(data, rows, k, x.dtype)
+
+
+def q8_pack(codes, scales, *, dtype=torch.float32, stream=None):
+    """Lays out codes int8 [rows, in_features] and scales float32 [rows] for matmul_q8: value (r, k) is
+    codes[r, k] * scales[r]. ``dtype``: of the output where the rows are a product's tokens."""
+    if codes.dim() != 2:
+        _fail("codes", "must be [rows, in_features]")
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    _storage(scales, "scales")
+    rows, k = codes.shape
+    cp = _dense("codes", codes, (rows, k), torch.int8, scales.device)
+    sp = _dense("scales", scales, (rows,), torch.float32, codes.device)
+    data = _q8_new(rows, k, codes.device, stream)
+    with torch.cuda.device(codes.device):
+        _check(_load().q8_pack(cp, sp, data.data_ptr(), rows, k,
+                               _raw_stream(codes.device.index) if stream is None else stream.cuda_stream))
+    return Q8Rows(data, rows, k, dtype)
+
+
+def q8_unpack(q, *, stream=None):
+    """The codes (int8 [rows, in_features]) and scales (float32 [rows]) of Q8Rows."""
+    codes = _new((q.rows, q.in_features), torch.int8, q.device, stream)
+    scales = _new((q.rows,), torch.float32, q.device, stream)
+    with torch.cuda.device(q.device):
+        _check(_load().q8_unpack(q.data.data_ptr(), codes.data_ptr(), scales.data_ptr(), q.rows, q.in_features,
+                                 _raw_stream(q.device.index) if stream is None else stream.cuda_stream))
+    return codes, scales
+
+
+def matmul_q8(x, weights, bias=None, alpha=None, residual=None, *, act="none", res_before_act=False, out=None, stream=None,
+              workspace=None):
+    """y = epilogue(x @ W^T) in 8-bit integers, with weights from q8_pack or quantize_rows (a row for
+    each output).
+
+    x [rows, in_features]: float32, bfloat16 or float16, rows at any stride, quantized by the call
+    as quantize_rows does (in the workspace: no ``workspace=False``), or Q8Rows. residual [rows,
+    out_features] in x's dtype, rows at any stride; bias, alpha (act="prelu"): float32
+    [out_features]. The epilogue is conv2d_fused's. The sums are exact. Returns y [rows,
+    out_features] in x's dtype."""
+    packed = isinstance(x, Q8Rows)
+    dev, dtype, n, k = weights.device, x.dtype, weights.rows, weights.in_features
+    if packed:
+        dt, rows, xp, x_row, qp = _DTYPES[dtype], x.rows, 0, 0, x.data.data_ptr()
+        if x.in_features != k or x.device != dev:
+            _fail("x", f"has {x.in_features} inputs on {x.device}, expected {k} on {dev}")
+    else:
+        dt = _storage(x)
+        if x.dim() != 2:
+            _fail("x", "must be [rows, in_features]")
+        rows, x_row, qp = x.shape[0], x.stride(0), 0
+        xp = _rows("x", x, (rows, k), dtype, dev)
+    bp = _dense("bias", bias, (n,), torch.float32, dev)
+    ap = _dense("alpha", alpha, (n,), torch.float32, dev)
+    rp = 0 if residual is None else _rows("residual", residual, (rows, n), dtype, dev)
+    if out is None:
+        out = _new((rows, n), dtype, dev, stream)
+        yp = out.data_ptr()
+    else:
+        yp = _rows("out", out, (rows, n), dtype, dev)
+    args = _Q8.pack(xp, qp, weights.data.data_ptr(), bp, ap, rp, yp, x_row, 0 if residual is None else residual.stride(0),
+                    out.stride(0), rows, k, n, _act(act) | (RES_BEFORE_ACT if res_before_act else 0), dt)
+    if not packed:
+        need = 0
+        if workspace is None:
+            size = ctypes.c_size_t(0)
+            _check(_load().matmul_q8_workspace_size(args, ctypes.byref(size)))
+            need = size.value
+        _scratch(dev, stream, workspace, need)
+    _call("matmul_q8", args, dev, stream)
     return out

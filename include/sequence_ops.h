@@ -216,6 +216,51 @@ typedef struct matvec_w4_args {
 
 int matvec_w4(const matvec_w4_args *args, void *stream);
 
+/* Rows in 8 bits: value (r, k) is scale[r] * code, with a code of -128 .. 127. They are laid out
+ * for matmul_q8, which takes activations (a row for each token) and weights (a row for each
+ * output) alike: `packed` is 16-byte aligned and q8_packed_bytes() long, and depends on the
+ * number of rows. in_features is at most 2^17 - 1, so that sums of products fit 32 bits.
+ * quantize_rows chooses, for each row, the scale max(|x|) / 127 (rounded to fp32, at least
+ * 2^-126) and the codes x / scale, rounded to the nearest whole number, ties to even, with no
+ * error but that. A row with an infinity or a NaN gets a scale of NaN and codes of 0.
+ * q8_pack lays out given codes (int8 [rows, in_features], contiguous) and scales (fp32 [rows]);
+ * q8_unpack gives both back. */
+typedef struct quantize_rows_args {
+    const void *x;         /* [rows, in_features], rows x_row elements apart */
+    void *packed;
+    long long x_row;
+    int rows, in_features;
+    int dtype;             /* of x */
+} quantize_rows_args;
+
+int q8_packed_bytes(int rows, int in_features, size_t *bytes);
+int quantize_rows(const quantize_rows_args *args, void *stream);
+int q8_pack(const void *codes, const float *scales, void *packed, int rows, int in_features, void *stream);
+int q8_unpack(const void *packed, void *codes, float *scales, int rows, int in_features, void *stream);
+
+/* y[r, o] = epilogue(scale_x[r] * scale_w[o] * sum_k code_x[r, k] * code_w[o, k]) for `rows` token
+ * rows, the epilogue that of conv2d_fused: bias, activation, and a residual before or after it.
+ * The sums are exact; what follows is fp32, rounded once to y. The rows are x, quantized by the
+ * call as quantize_rows does (it needs matmul_q8_workspace_size() bytes of workspace, or returns
+ * CONV2D_EUNSUPPORTED), or x_packed, for several products of the same rows. A row or an output
+ * whose scale is NaN gives NaN. */
+typedef struct matmul_q8_args {
+    const void *x;         /* [rows, in_features], rows x_row elements apart, or NULL */
+    const void *x_packed;  /* where x is NULL: packed rows, with the same sizes */
+    const void *weights;   /* out_features packed rows of in_features */
+    const float *bias;     /* [out_features] or NULL */
+    const float *alpha;    /* [out_features], needed by CONV2D_ACT_PRELU */
+    const void *residual;  /* [rows, out_features], rows residual_row elements apart, or NULL */
+    void *y;               /* [rows, out_features], rows y_row elements apart */
+    long long x_row, residual_row, y_row;
+    int rows, in_features, out_features;
+    int act;               /* CONV2D_ACT_*, CONV2D_RES_BEFORE_ACT */
+    int dtype;             /* of x, residual and y */
+} matmul_q8_args;
+
+int matmul_q8(const matmul_q8_args *args, void *stream);
+int matmul_q8_workspace_size(const matmul_q8_args *args, size_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif
