@@ -247,6 +247,7 @@ size_t q8_bytes(int rows, int in_features);
 hipError_t launch_quantize_rows(const quantize_rows_args &a, hipStream_t st);
 hipError_t launch_q8_pack(const void *codes, const float *scales, void *packed, int rows, int in_features, hipStream_t st);
 hipError_t launch_q8_unpack(const void *packed, void *codes, float *scales, int rows, int in_features, hipStream_t st);
-hipError_t launch_matmul_q8(const matmul_q8_args &a, void *ws, hipStream_t st);  // ws: q8_bytes for x
+bool q8_in_one(const matmul_q8_args &a);  // x, not quantized, needs no workspace
+hipError_t launch_matmul_q8(const matmul_q8_args &a, void *ws, hipStream_t st);  // ws: else q8_bytes for x
 
 }  // namespace c2d

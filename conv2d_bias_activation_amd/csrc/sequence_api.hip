@@ -366,7 +366,7 @@ int check_matmul_q8(const matmul_q8_args *args, const char *op) {
          Extent{"alpha", (a.act & 0xff) == CONV2D_ACT_PRELU ? a.alpha : nullptr, 4ll * a.out_features}});
 }
 
-size_t q8_need(const matmul_q8_args &a) { return a.rows && a.x ? q8_bytes(a.rows, a.in_features) : 0; }
+size_t q8_need(const matmul_q8_args &a) { return a.rows && a.x && !q8_in_one(a) ? q8_bytes(a.rows, a.in_features) : 0; }
 
 bool type16(int dtype) { return dtype == CONV2D_DTYPE_BF16 || dtype == CONV2D_DTYPE_F16; }
 

@@ -521,7 +521,7 @@ def matmul_q8(x, weights, bias=None, alpha=None, residual=None, *, act="none", r
     each output).
 
     x [rows, in_features]: float32, bfloat16 or float16, rows at any stride, quantized by the call
-    as quantize_rows does (in the workspace: no ``workspace=False``), or Q8Rows. residual [rows,
+    as quantize_rows does (in the workspace, but for up to 4 rows of up to 8192 inputs), or Q8Rows. residual [rows,
     out_features] in x's dtype, rows at any stride; bias, alpha (act="prelu"): float32
     [out_features]. The epilogue is conv2d_fused's. The sums are exact. Returns y [rows,
     out_features] in x's dtype."""
@@ -553,6 +553,7 @@ def matmul_q8(x, weights, bias=None, alpha=None, residual=None, *, act="none", r
             size = ctypes.c_size_t(0)
             _check(_load().matmul_q8_workspace_size(args, ctypes.byref(size)))
             need = size.value
-        _scratch(dev, stream, workspace, need)
+        if need or workspace is not None:
+            _scratch(dev, stream, workspace, need)
     _call("matmul_q8", args, dev, stream)
     return out

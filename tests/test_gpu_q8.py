@@ -150,6 +150,11 @@ PRODUCTS = [  # type, rows, inputs, outputs, what else
     ("bf16", 3, 131071, 20, {}),
     ("f32", 90, 131071, 70, {}),
     ("f16", 1030, 20000, 260, {}),
+    ("f32", 4, 8192, 100, {"bias": True, "residual": True, "act": "prelu"}),
+    ("bf16", 3, 4010, 16400, {"wide": 1, "shift": 1}),
+    ("f16", 1, 8191, 16391, {"residual": True, "before": True}),
+    ("bf16", 4, 8193, 40, {}),
+    ("f16", 2, 17, 5, {"act": "silu"}),
 ]
 
 
@@ -259,10 +264,11 @@ def test_offsets_past_32_bits():
 
 
 def test_product_needs_a_workspace_or_packed_rows():
-    x = _on(_normal(1, 4, 64))
+    x = _on(_normal(1, 20, 64))
     w = c2d.q8_pack(*map(_on, _weights(1, 8, 64)))
     with pytest.raises(c2d.Conv2dError, match="needs a workspace"):
         c2d.matmul_q8(x, w, workspace=False)
+    assert torch.equal(c2d.matmul_q8(x[:4], w, workspace=False), c2d.matmul_q8(x, w)[:4])  # a few rows need none
     with pytest.raises(ValueError, match="inputs"):
         c2d.matmul_q8(c2d.quantize_rows(x[:, :32]), w)
     assert c2d.matmul_q8(x[:0], w).shape == (0, 8)

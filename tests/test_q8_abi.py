@@ -68,6 +68,7 @@ def test_sizes():
     assert size(17, 1 << 17, ctypes.byref(n)) == c2d.EUNSUPPORTED
     assert size(17, 0, ctypes.byref(n)) == c2d.EINVAL and size(17, 1, None) == c2d.EINVAL
     assert _matmul(size=True, rows=17) >= 2 * 4 * 1024 + 128
+    assert _matmul(size=True, rows=4) == 0 and _matmul(size=True, rows=4, in_features=8193, x_row=8193) > 0
     assert _matmul(size=True, x=0, x_packed=4 * G) == 0 and _matmul(size=True, rows=0) == 0
 
 
@@ -88,7 +89,7 @@ def test_pack_refusals():
 
 def test_too_small_a_workspace_is_refused_by_name():
     c2d._load().conv2d_set_workspace(None, 0)
-    assert _matmul() == c2d.EUNSUPPORTED
+    assert _matmul(rows=40) == c2d.EUNSUPPORTED
     assert "needs a workspace" in c2d.last_error()
 
 
@@ -99,7 +100,7 @@ def test_nothing_to_do_is_fine_without_a_device():
 
 @pytest.mark.skipif(torch.cuda.device_count() > 0, reason="needs a machine without a GPU")
 def test_no_device_returns_ehip_not_a_crash():
-    for call in (_rows, lambda: _matmul(x=0, x_packed=4 * G), lambda: _matmul(x=0, x_packed=4 * G, rows=2000, y_row=600),
+    for call in (_rows, _matmul, lambda: _matmul(x=0, x_packed=4 * G), lambda: _matmul(x=0, x_packed=4 * G, rows=2000, y_row=600),
                  lambda: c2d._load().q8_pack(G, 2 * G, 3 * G, 16, 64, None),
                  lambda: c2d._load().q8_unpack(G, 2 * G, 3 * G, 16, 64, None)):
         assert call() == c2d.EHIP
