@@ -9,7 +9,7 @@
 // The gradient carried towards the first token, c_t = f_t g_t with g_t = e_t + c_{t+1} and e the
 // part of h_t's gradient that comes from y_t, is the same scan backwards: c -> A c + D.
 #include <algorithm>
-#include <initializer_list>
+#include <type_traits>
 
 #include "kernels.hpp"
 #include "runtime.hpp"
@@ -21,13 +21,13 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// sigmoid(z) and 1 - sigmoid(z), both to full relative precision.
-__device__ __forceinline__ void gates(float z, float &keep, float &take) {
-    const float t = __builtin_amdgcn_exp2f(-fabsf(z) * kLog2e);
-    const float large = __builtin_amdgcn_rcpf(1.0f + t);
-    const float small = t * large;
-    keep = z >= 0.0f ? large : small;
-    take = z >= 0.0f ? small : large;
+// keep = sigmoid(z) and take = 1 - sigmoid(z) for z = v + bias, scaled = -log2(e) bias; both to
+// full relative precision. Where exp(-z) is infinite its product with 0 is not a number, of which
+// the minimum with 1 is 1, as it should be; a z that is not a number makes keep one too.
+__device__ __forceinline__ void gates(float v, float scaled, float &keep, float &take) {
+    const float t = __builtin_amdgcn_exp2f(fmaf(v, -kLog2e, scaled));
+    keep = __builtin_amdgcn_rcpf(1.0f + t);
+    take = fminf(t * keep, 1.0f);
 }
 
 constexpr int kTW = 8;          // neighbouring tokens of a wave
@@ -90,11 +90,38 @@ template <typename T> __device__ __forceinline__ T *rows(void *p, const Place &w
 
 template <int VEC> using Floats = Pack<float, VEC>;
 
+// A lane's channels: c to c + VEC - 1, of which it owns the last `own` (0: it only follows). The last
+// lane of an odd number of channels takes the last two and owns one.
+struct Channels {
+    int c, own;
+};
+template <int VEC> __device__ __forceinline__ Channels channels_of(int ch, int channels) {
+    if (ch + VEC <= channels) return {ch, VEC};
+    return {channels - VEC, ch < channels ? channels - ch : 0};
+}
+
+// Rows need not be aligned to more than their type.
+template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> get(const T *p) {
+    Pack<T, VEC> v;
+    __builtin_memcpy(&v, p, sizeof v);
+    return v;
+}
+template <typename T, int VEC> __device__ __forceinline__ void put(T *p, const Pack<T, VEC> &v, int own = VEC) {
+    static_assert(VEC <= 2);
+    if (own == VEC)
+        __builtin_memcpy(p, &v, sizeof v);
+    else if (VEC == 2 && own == 1)
+        p[VEC - 1] = v.v[VEC - 1];
+}
+
+// Whether every lane of a wave owns all its channels.
+template <int VEC> __device__ __forceinline__ bool all_own(int own) { return __all(own == VEC); }
+
 // kTW tokens from t on of token rows, the last row again from `end` on.
 template <typename T, int VEC>
 __device__ __forceinline__ void fetch(Pack<T, VEC> (&v)[kTW], const T *p, long long token, int t, int end, int c) {
 #pragma unroll
-    for (int i = 0; i < kTW; i++) v[i] = load_pack<T, VEC>(p + min(t + i, end - 1) * token + (unsigned)c);
+    for (int i = 0; i < kTW; i++) v[i] = get<T, VEC>(p + min(t + i, end - 1) * token + (unsigned)c);
 }
 
 // Composite of the records from lo on and before hi (towards later tokens, or earlier ones), the
@@ -112,8 +139,8 @@ __device__ __forceinline__ Floats<VEC> fold(const float *rec, long long stride, 
         for (int i = 0; i < 4; i++) {
             const int j = min(j0 + i, n - 1);
             const float *p = rec + (BACK ? first + n - 1 - j : first + j) * stride + c;
-            ra[i] = load_pack<float, VEC>(p + kA * (long long)channels);
-            rb[i] = load_pack<float, VEC>(p + (BACK ? kD : kB) * (long long)channels);
+            ra[i] = get<float, VEC>(p + kA * (long long)channels);
+            rb[i] = get<float, VEC>(p + (BACK ? kD : kB) * (long long)channels);
         }
 #pragma unroll
         for (int i = 0; i < 4; i++) {
@@ -142,57 +169,122 @@ __device__ __forceinline__ Floats<VEC> fold(const float *rec, long long stride, 
 
 // ---------------------------------------------------------------------------- prompts
 
-// FIRST: the first pass over split sequences, which leaves the chunks' records; else the pass
-// that writes y and the states.
-template <typename T, int VEC, bool FIRST>
-__global__ __launch_bounds__(64 * kNW) void rec_prompt_kernel(const gated_recurrence_args a, const RecCut k) {
+// The first pass over split sequences, which leaves the chunks' records. A wave takes an eighth of
+// the chunk and needs the others at the end only.
+template <typename T, int VEC, bool COUPLED>
+__global__ __launch_bounds__(64 * kNW) void rec_first_kernel(const gated_recurrence_args a, const RecCut k) {
+    __shared__ float2 s_run[kNW][VEC][64];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int item = blockIdx.x / k.cblocks;
+    const auto [c, own] = channels_of<VEC>(((int)(blockIdx.x % k.cblocks) * 64 + lane) * VEC, a.channels);
+    Place p;
+    if (!place_of(a, k, item, p) || p.chunk == p.last) return;  // so the chunk is a whole run
+    const T *x = rows<T>(a.x, p, a.x_batch, a.x_token), *forget = rows<T>(a.forget, p, a.forget_batch, a.forget_token);
+    const long long stride = 2ll * a.channels;
+    Floats<VEC> h{};
+    if (p.chunk == 0 && wave == 0) {
+        const int row = state_row(a.state, a.slots, p.r.seq, a.state_rows);
+        if (row >= 0 && !a.fresh) h = get<float, VEC>(a.state + (long long)row * a.channels + c);
+        put<float, VEC>(k.rec + (item + p.last) * stride + kB * (long long)a.channels + c, h, own);
+    }
+    float bias[VEC] = {};
+#pragma unroll
+    for (int v = 0; v < VEC; v++) bias[v] = a.forget_bias ? -kLog2e * a.forget_bias[c + v] : 0.0f;
+    float At[VEC], Bt[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; v++) At[v] = 1.0f, Bt[v] = 0.0f;
+    const int part = k.run / kNW, t0 = p.r.first + wave * part, t1 = t0 + part;
+    Pack<T, VEC> nx[kTW], nf[kTW];
+    fetch<T, VEC>(nf, forget, a.forget_token, t0, t1, c);
+    fetch<T, VEC>(nx, x, a.x_token, t0, t1, c);
+    for (int t = t0; t < t1; t += kTW) {
+        float f[kTW][VEC], b[kTW][VEC];
+#pragma unroll
+        for (int i = 0; i < kTW; i++)
+#pragma unroll
+            for (int v = 0; v < VEC; v++) {
+                float take;
+                gates(to_f32(nf[i].v[v]), bias[v], f[i][v], take);
+                b[i][v] = COUPLED ? to_f32(nx[i].v[v]) * take : to_f32(nx[i].v[v]);
+            }
+        if (t + kTW < t1) {
+            fetch<T, VEC>(nf, forget, a.forget_token, t + kTW, t1, c);
+            fetch<T, VEC>(nx, x, a.x_token, t + kTW, t1, c);
+        }
+#pragma unroll
+        for (int i = 0; i < kTW; i++)
+#pragma unroll
+            for (int v = 0; v < VEC; v++) {
+                Bt[v] = fmaf(f[i][v], Bt[v], b[i][v]);
+                At[v] *= f[i][v];
+            }
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; v++) s_run[wave][v][lane] = float2{At[v], Bt[v]};
+    __syncthreads();
+    if (wave != 0) return;
+    Floats<VEC> decay;
+#pragma unroll
+    for (int v = 0; v < VEC; v++) decay.v[v] = p.chunk == 0 ? 0.0f : 1.0f;
+#pragma unroll
+    for (int w = 0; w < kNW; w++)
+#pragma unroll
+        for (int v = 0; v < VEC; v++) {
+            const float2 m = s_run[w][v][lane];
+            h.v[v] = fmaf(m.x, h.v[v], m.y);
+            decay.v[v] *= m.x;
+        }
+    float *q = k.rec + item * stride + c;
+    put<float, VEC>(q + kA * (long long)a.channels, decay, own);
+    put<float, VEC>(q + kB * (long long)a.channels, h, own);
+}
+
+// The pass that writes y and the states.
+template <typename T, int VEC, bool COUPLED, bool GATED>
+__global__ __launch_bounds__(64 * kNW, 4) void rec_prompt_kernel(const gated_recurrence_args a, const RecCut k) {
     __shared__ float2 s_run[2][kNW][VEC][64];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     // the second pass takes the chunks that the first read last first: they may still be cached
-    const int item = FIRST ? blockIdx.x / k.cblocks : k.items - 1 - blockIdx.x / k.cblocks;
-    const int ch = (int)(blockIdx.x % k.cblocks) * 64 * VEC + lane * VEC;
-    const bool on = ch < a.channels;
-    const int c = on ? ch : a.channels - VEC;
+    const int item = k.items - 1 - blockIdx.x / k.cblocks;
+    const auto [c, own] = channels_of<VEC>(((int)(blockIdx.x % k.cblocks) * 64 + lane) * VEC, a.channels);
     Place p;
     if (!place_of(a, k, item, p)) return;
-    if (FIRST && p.chunk == p.last) return;
 
     const T *x = rows<T>(a.x, p, a.x_batch, a.x_token), *forget = rows<T>(a.forget, p, a.forget_batch, a.forget_token);
-    const T *gate = a.gate ? rows<T>(a.gate, p, a.gate_batch, a.gate_token) : nullptr;
+    const T *gate = GATED ? rows<T>(a.gate, p, a.gate_batch, a.gate_token) : nullptr;
     T *y = rows<T>(a.y, p, a.y_batch, a.y_token);
     const int row = state_row(a.state, a.slots, p.r.seq, a.state_rows);
     float *state = row < 0 ? nullptr : a.state + (long long)row * a.channels + c;
     const long long stride = 2ll * a.channels;
 
     Floats<VEC> bias{}, h{};
-    if (a.forget_bias) bias = load_pack<float, VEC>(a.forget_bias + c);
-    if (p.chunk == 0 && (FIRST || p.last == 0) && state && !a.fresh) h = load_pack<float, VEC>(state);
-    if (FIRST && p.chunk == 0 && wave == 0 && on)
-        store_pack<float, VEC>(k.rec + (item + p.last) * stride + kB * (long long)a.channels + c, h);
+    if (a.forget_bias) bias = get<float, VEC>(a.forget_bias + c);
+#pragma unroll
+    for (int v = 0; v < VEC; v++) bias.v[v] *= -kLog2e;
+    if (p.last == 0 && state && !a.fresh) h = get<float, VEC>(state);
 
     Pack<T, VEC> nx[kTW], nf[kTW], ng[kTW];
     auto next = [&](int t0) {
         const int t = t0 + wave * kTW;
         fetch<T, VEC>(nx, x, a.x_token, t, p.end, c);
         fetch<T, VEC>(nf, forget, a.forget_token, t, p.end, c);
-        if (!FIRST && gate) fetch<T, VEC>(ng, gate, a.gate_token, t, p.end, c);
+        if (GATED) fetch<T, VEC>(ng, gate, a.gate_token, t, p.end, c);
     };
     if (p.end > p.r.first) next(p.r.first);
-    if (!FIRST && p.last > 0) {
+    if (p.last > 0) {
         const float *rec = k.rec + (item - p.chunk) * stride;
         if (p.chunk == 0)
-            h = load_pack<float, VEC>(rec + p.last * stride + kB * (long long)a.channels + c);
+            h = get<float, VEC>(rec + p.last * stride + kB * (long long)a.channels + c);
         else
             h = fold<VEC, false>(rec, stride, a.channels, 0, p.chunk, c, wave, lane, s_run[0]);
     }
-    float decay[VEC];  // FIRST: of the chunk so far
-#pragma unroll
-    for (int v = 0; v < VEC; v++) decay[v] = 1.0f;
 
     int buf = 0;
-    for (int t0 = p.r.first; t0 < p.end; t0 += kTile, buf ^= 1) {
+    auto tile = [&](int t0, auto full) {
+        constexpr bool kFull = decltype(full)::value;
         const int t = t0 + wave * kTW;
-        float f[kTW][VEC], b[kTW][VEC], z[kTW][VEC], A[VEC], B[VEC];
+        float f[kTW][VEC], b[kTW][VEC], A[VEC], B[VEC];
+        Pack<T, VEC> g[kTW];
 #pragma unroll
         for (int v = 0; v < VEC; v++) A[v] = 1.0f, B[v] = 0.0f;
 #pragma unroll
@@ -200,13 +292,13 @@ __global__ __launch_bounds__(64 * kNW) void rec_prompt_kernel(const gated_recurr
 #pragma unroll
             for (int v = 0; v < VEC; v++) {
                 float take;
-                gates(to_f32(nf[i].v[v]) + bias.v[v], f[i][v], take);
-                b[i][v] = to_f32(nx[i].v[v]) * (a.coupled ? take : 1.0f);
-                if (t + i >= p.end) f[i][v] = 1.0f, b[i][v] = 0.0f;
+                gates(to_f32(nf[i].v[v]), bias.v[v], f[i][v], take);
+                b[i][v] = COUPLED ? to_f32(nx[i].v[v]) * take : to_f32(nx[i].v[v]);
+                if (!kFull && t + i >= p.end) f[i][v] = 1.0f, b[i][v] = 0.0f;
                 B[v] = fmaf(f[i][v], B[v], b[i][v]);
                 A[v] *= f[i][v];
-                if (!FIRST) z[i][v] = gate ? activate_c<CONV2D_ACT_SILU>(to_f32(ng[i].v[v]), 0.0f) : 1.0f;
             }
+            if (GATED) g[i] = ng[i];
         }
         if (t0 + kTile < p.end) next(t0 + kTile);
 #pragma unroll
@@ -220,73 +312,71 @@ __global__ __launch_bounds__(64 * kNW) void rec_prompt_kernel(const gated_recurr
                 if (w == wave) from[v] = h.v[v];
                 const float2 m = s_run[buf][w][v][lane];
                 h.v[v] = fmaf(m.x, h.v[v], m.y);
-                if (FIRST) decay[v] *= m.x;
             }
-        if (FIRST) continue;
+        buf ^= 1;
 #pragma unroll
         for (int i = 0; i < kTW; i++) {
             Pack<T, VEC> out;
 #pragma unroll
             for (int v = 0; v < VEC; v++) {
                 from[v] = fmaf(f[i][v], from[v], b[i][v]);
-                out.v[v] = round_fp32<T>(from[v] * z[i][v]);
+                const float z = GATED ? activate_c<CONV2D_ACT_SILU>(to_f32(g[i].v[v]), 0.0f) : 1.0f;
+                out.v[v] = round_fp32<T>(GATED ? from[v] * z : from[v]);
             }
-            if (on && t + i < p.end) store_pack<T, VEC>(y + (t + i) * a.y_token + (unsigned)c, out);
+            if (kFull)
+                put<T, VEC>(y + (t + i) * a.y_token + (unsigned)c, out);
+            else if (t + i < p.end)
+                put<T, VEC>(y + (t + i) * a.y_token + (unsigned)c, out, own);
         }
-    }
-    if (!on || wave != 0) return;
-    if (FIRST) {
-        float *q = k.rec + item * stride + c;
-        Floats<VEC> A;
-#pragma unroll
-        for (int v = 0; v < VEC; v++) A.v[v] = p.chunk == 0 ? 0.0f : decay[v];
-        store_pack<float, VEC>(q + kA * (long long)a.channels, A);
-        store_pack<float, VEC>(q + kB * (long long)a.channels, h);
-    } else if (state && p.chunk == p.last) {
-        store_pack<float, VEC>(state, h);
-    }
+    };
+    int t0 = p.r.first;
+    if (all_own<VEC>(own))
+        for (; t0 + kTile <= p.end; t0 += kTile) tile(t0, std::true_type{});
+    for (; t0 < p.end; t0 += kTile) tile(t0, std::false_type{});
+    if (wave == 0 && state && p.chunk == p.last) put<float, VEC>(state, h, own);
 }
 
 // ---------------------------------------------------------------------------- gradient
 
 // The first pass of the gradient walks forwards: it leaves, for each tile, the state before it as
 // an affine map of the state before the chunk, and, for split sequences, the chunks' records.
-template <typename T, int VEC>
+template <typename T, int VEC, bool WHOLE, bool GATED, bool SPLIT>
 __global__ __launch_bounds__(64 * kNW) void rec_back_first_kernel(const gated_recurrence_backward_args a, const RecCut k) {
     __shared__ float4 s_run[2][kNW][VEC][64];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int item = blockIdx.x / k.cblocks;
-    const int ch = (int)(blockIdx.x % k.cblocks) * 64 * VEC + lane * VEC;
-    const bool on = ch < a.channels;
-    const int c = on ? ch : a.channels - VEC;
+    // WHOLE: the channels fill their blocks
+    const auto [c, own] = channels_of<VEC>(((int)(blockIdx.x % k.cblocks) * 64 + lane) * VEC, a.channels);
     Place p;
     if (!place_of(a, k, item, p)) return;
     const bool split = p.last > 0;
 
     const T *x = rows<T>(a.x, p, a.x_batch, a.x_token), *forget = rows<T>(a.forget, p, a.forget_batch, a.forget_token);
-    const T *gate = a.gate ? rows<T>(a.gate, p, a.gate_batch, a.gate_token) : nullptr;
+    const T *gate = GATED ? rows<T>(a.gate, p, a.gate_batch, a.gate_token) : nullptr;
     const T *grad = rows<T>(a.grad, p, a.grad_batch, a.grad_token);
     const long long tiles = a.offsets ? 0 : (a.tokens + kTile - 1) / kTile;
     float *tile = k.tile + (a.offsets ? p.start / kTile + p.r.seq : p.r.seq * tiles) * 2 * a.channels + c;
 
     Floats<VEC> bias{}, h{}, carry{};
-    if (a.forget_bias) bias = load_pack<float, VEC>(a.forget_bias + c);
+    if (a.forget_bias) bias = get<float, VEC>(a.forget_bias + c);
+#pragma unroll
+    for (int v = 0; v < VEC; v++) bias.v[v] *= -kLog2e;
     if (p.chunk == 0) {
         const int row = state_row(a.state, a.slots, p.r.seq, a.state_rows);
-        if (row >= 0) h = load_pack<float, VEC>(a.state + (long long)row * a.channels + c);
+        if (row >= 0) h = get<float, VEC>(a.state + (long long)row * a.channels + c);
     }
     if (split && p.chunk == p.last) {
         const int row = state_row(a.grad_state, a.slots, p.r.seq, a.state_rows);
-        if (row >= 0) carry = load_pack<float, VEC>(a.grad_state + (long long)row * a.channels + c);
+        if (row >= 0) carry = get<float, VEC>(a.grad_state + (long long)row * a.channels + c);
     }
     Pack<T, VEC> nx[kTW], nf[kTW], ng[kTW], ne[kTW];
     auto next = [&](int t0) {
         const int t = t0 + wave * kTW;
         fetch<T, VEC>(nx, x, a.x_token, t, p.end, c);
         fetch<T, VEC>(nf, forget, a.forget_token, t, p.end, c);
-        if (split) {
+        if (SPLIT) {
             fetch<T, VEC>(ne, grad, a.grad_token, t, p.end, c);
-            if (gate) fetch<T, VEC>(ng, gate, a.gate_token, t, p.end, c);
+            if constexpr (GATED) fetch<T, VEC>(ng, gate, a.gate_token, t, p.end, c);
         }
     };
     if (p.end > p.r.first) next(p.r.first);
@@ -295,14 +385,14 @@ __global__ __launch_bounds__(64 * kNW) void rec_back_first_kernel(const gated_re
     for (int v = 0; v < VEC; v++) decay[v] = 1.0f, D[v] = 0.0f;
 
     int buf = 0;
-    for (int t0 = p.r.first; t0 < p.end; t0 += kTile, buf ^= 1) {
-        if (wave == 0 && on) {
+    for (int t0 = p.r.first; t0 < p.end; t0 += kTile) {
+        if (wave == 0) {
             float *q = tile + (t0 / kTile) * 2ll * a.channels;
             Floats<VEC> A;
 #pragma unroll
             for (int v = 0; v < VEC; v++) A.v[v] = p.chunk == 0 ? 0.0f : decay[v];
-            store_pack<float, VEC>(q, A);
-            store_pack<float, VEC>(q + a.channels, h);
+            put<float, VEC>(q, A, own);
+            put<float, VEC>(q + a.channels, h, own);
         }
         const int t = t0 + wave * kTW;
         float A[VEC], B[VEC], E[VEC];
@@ -313,35 +403,38 @@ __global__ __launch_bounds__(64 * kNW) void rec_back_first_kernel(const gated_re
 #pragma unroll
             for (int v = 0; v < VEC; v++) {
                 float f, take;
-                gates(to_f32(nf[i].v[v]) + bias.v[v], f, take);
+                gates(to_f32(nf[i].v[v]), bias.v[v], f, take);
                 float b = to_f32(nx[i].v[v]) * (a.coupled ? take : 1.0f);
                 if (t + i >= p.end) f = 1.0f, b = 0.0f;
                 B[v] = fmaf(f, B[v], b);
                 A[v] *= f;
-                if (split) {
+                if (SPLIT) {
                     float e = to_f32(ne[i].v[v]);
-                    if (gate) e *= activate_c<CONV2D_ACT_SILU>(to_f32(ng[i].v[v]), 0.0f);
+                    if constexpr (GATED) e *= activate_c<CONV2D_ACT_SILU>(to_f32(ng[i].v[v]), 0.0f);
                     if (t + i >= p.end) e = 0.0f;
                     E[v] = fmaf(A[v], e, E[v]);
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
         if (t0 + kTile < p.end) next(t0 + kTile);
 #pragma unroll
         for (int v = 0; v < VEC; v++) s_run[buf][wave][v][lane] = float4{A[v], B[v], E[v], 0.0f};
         __syncthreads();
+        const auto *runs = s_run[buf];
+        buf ^= 1;
         if (wave != 0) continue;
 #pragma unroll
         for (int w = 0; w < kNW; w++)
 #pragma unroll
             for (int v = 0; v < VEC; v++) {
-                const float4 m = s_run[buf][w][v][lane];
+                const float4 m = runs[w][v][lane];
                 h.v[v] = fmaf(m.x, h.v[v], m.y);
                 D[v] = fmaf(decay[v], m.z, D[v]);
                 decay[v] *= m.x;
             }
     }
-    if (!split || !on || wave != 0) return;
+    if (!split || wave != 0) return;
     float *q = k.rec + item * 3ll * a.channels + c;
     Floats<VEC> A, B, E;
     const bool last = p.chunk == p.last;
@@ -351,53 +444,53 @@ __global__ __launch_bounds__(64 * kNW) void rec_back_first_kernel(const gated_re
         B.v[v] = last ? carry.v[v] : h.v[v];
         E.v[v] = last ? fmaf(decay[v], carry.v[v], D[v]) : D[v];
     }
-    store_pack<float, VEC>(q + kA * (long long)a.channels, A);
-    store_pack<float, VEC>(q + kB * (long long)a.channels, B);
-    store_pack<float, VEC>(q + kD * (long long)a.channels, E);
+    put<float, VEC>(q + kA * (long long)a.channels, A, own);
+    put<float, VEC>(q + kB * (long long)a.channels, B, own);
+    put<float, VEC>(q + kD * (long long)a.channels, E, own);
 }
 
 // The second pass walks backwards over the tiles and writes the gradients.
-template <typename T, int VEC>
+template <typename T, int VEC, bool WHOLE, bool GATED>
 __global__ __launch_bounds__(64 * kNW) void rec_back_kernel(const gated_recurrence_backward_args a, const RecCut k) {
     __shared__ float4 s_run[2][kNW][VEC][64];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int item = k.items - 1 - blockIdx.x / k.cblocks;
-    const int ch = (int)(blockIdx.x % k.cblocks) * 64 * VEC + lane * VEC;
-    const bool on = ch < a.channels;
-    const int c = on ? ch : a.channels - VEC;
+    const auto [c, own] = channels_of<VEC>(((int)(blockIdx.x % k.cblocks) * 64 + lane) * VEC, a.channels);
     float sum[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; v++) sum[v] = 0.0f;
     Place p;
     if (!place_of(a, k, item, p)) {
-        if (k.bias && wave == 0 && on) store_pack<float, VEC>(k.bias + item * (long long)a.channels + c, Floats<VEC>{});
+        if (k.bias && wave == 0) put<float, VEC>(k.bias + item * (long long)a.channels + c, Floats<VEC>{}, own);
         return;
     }
     const T *x = rows<T>(a.x, p, a.x_batch, a.x_token), *forget = rows<T>(a.forget, p, a.forget_batch, a.forget_token);
-    const T *gate = a.gate ? rows<T>(a.gate, p, a.gate_batch, a.gate_token) : nullptr;
+    const T *gate = GATED ? rows<T>(a.gate, p, a.gate_batch, a.gate_token) : nullptr;
     const T *grad = rows<T>(a.grad, p, a.grad_batch, a.grad_token);
     T *gx = rows<T>(a.grad_x, p, a.grad_x_batch, a.grad_x_token);
     T *gf = rows<T>(a.grad_forget, p, a.grad_forget_batch, a.grad_forget_token);
-    T *gg = a.gate ? rows<T>(a.grad_gate, p, a.grad_gate_batch, a.grad_gate_token) : nullptr;
+    T *gg = GATED ? rows<T>(a.grad_gate, p, a.grad_gate_batch, a.grad_gate_token) : nullptr;
     const long long tiles = a.offsets ? 0 : (a.tokens + kTile - 1) / kTile;
     const float *tile = k.tile + (a.offsets ? p.start / kTile + p.r.seq : p.r.seq * tiles) * 2 * a.channels + c;
     const int row = state_row(a.grad_state, a.slots, p.r.seq, a.state_rows);
     float *grad_state = row < 0 ? nullptr : a.grad_state + (long long)row * a.channels + c;
 
     Floats<VEC> bias{}, before{}, carry{};  // state before the chunk, gradient carried into the tile
-    if (a.forget_bias) bias = load_pack<float, VEC>(a.forget_bias + c);
+    if (a.forget_bias) bias = get<float, VEC>(a.forget_bias + c);
+#pragma unroll
+    for (int v = 0; v < VEC; v++) bias.v[v] *= -kLog2e;
 
     Pack<T, VEC> nx[kTW], nf[kTW], ng[kTW], ne[kTW];
     Floats<VEC> na, nb;
     auto next = [&](int t0) {
         const int t = t0 + wave * kTW;
         const float *q = tile + (t0 / kTile) * 2ll * a.channels;
-        na = load_pack<float, VEC>(q);
-        nb = load_pack<float, VEC>(q + a.channels);
+        na = get<float, VEC>(q);
+        nb = get<float, VEC>(q + a.channels);
         fetch<T, VEC>(nx, x, a.x_token, t, p.end, c);
         fetch<T, VEC>(nf, forget, a.forget_token, t, p.end, c);
         fetch<T, VEC>(ne, grad, a.grad_token, t, p.end, c);
-        if (gate) fetch<T, VEC>(ng, gate, a.gate_token, t, p.end, c);
+        if constexpr (GATED) fetch<T, VEC>(ng, gate, a.gate_token, t, p.end, c);
     };
     const int final = p.end > p.r.first ? p.r.first + (p.end - 1 - p.r.first) / kTile * kTile : p.r.first - kTile;
     if (final >= p.r.first) next(final);
@@ -408,13 +501,13 @@ __global__ __launch_bounds__(64 * kNW) void rec_back_kernel(const gated_recurren
         if (p.chunk < p.last)
             carry = fold<VEC, true>(rec, 3ll * a.channels, a.channels, p.chunk + 1, p.last + 1, c, wave, lane, s);
         else
-            carry = load_pack<float, VEC>(rec + p.last * 3ll * a.channels + kB * (long long)a.channels + c);
+            carry = get<float, VEC>(rec + p.last * 3ll * a.channels + kB * (long long)a.channels + c);
     } else if (grad_state) {
-        carry = load_pack<float, VEC>(grad_state);
+        carry = get<float, VEC>(grad_state);
     }
 
     int buf = 0;
-    for (int t0 = final; t0 >= p.r.first; t0 -= kTile, buf ^= 1) {
+    for (int t0 = final; t0 >= p.r.first; t0 -= kTile) {
         const int t = t0 + wave * kTW;
         float xs[kTW][VEC], f[kTW][VEC], take[kTW][VEC], e[kTW][VEC], dz[kTW][VEC], A[VEC], B[VEC], D[VEC];
         float start[VEC];
@@ -428,13 +521,13 @@ __global__ __launch_bounds__(64 * kNW) void rec_back_kernel(const gated_recurren
 #pragma unroll
             for (int v = 0; v < VEC; v++) {
                 xs[i][v] = to_f32(nx[i].v[v]);
-                gates(to_f32(nf[i].v[v]) + bias.v[v], f[i][v], take[i][v]);
+                gates(to_f32(nf[i].v[v]), bias.v[v], f[i][v], take[i][v]);
                 e[i][v] = to_f32(ne[i].v[v]);
                 dz[i][v] = 0.0f;
-                if (gate) {
+                if constexpr (GATED) {
                     const float g = to_f32(ng[i].v[v]);
                     float up, down;
-                    gates(g, up, down);
+                    gates(g, 0.0f, up, down);
                     dz[i][v] = e[i][v] * up * fmaf(g, down, 1.0f);
                     e[i][v] *= g * up;
                 }
@@ -444,6 +537,7 @@ __global__ __launch_bounds__(64 * kNW) void rec_back_kernel(const gated_recurren
                 D[v] = fmaf(A[v] * f[i][v], e[i][v], D[v]);
                 A[v] *= f[i][v];
             }
+            __builtin_amdgcn_sched_barrier(0);  // token by token, as their loads arrive
         }
         if (t0 > p.r.first) next(t0 - kTile);
 #pragma unroll
@@ -488,28 +582,30 @@ __global__ __launch_bounds__(64 * kNW) void rec_back_kernel(const gated_recurren
                 cin[v] = g * f[i][v];
                 if (t + i < p.end) sum[v] += d;
             }
-            if (on && t + i < p.end) {
-                store_pack<T, VEC>(gx + (t + i) * a.grad_x_token + (unsigned)c, ox);
-                store_pack<T, VEC>(gf + (t + i) * a.grad_forget_token + (unsigned)c, of);
-                if (gate) store_pack<T, VEC>(gg + (t + i) * a.grad_gate_token + (unsigned)c, og);
+            if (t + i < p.end) {
+                const int part = WHOLE ? VEC : own;
+                put<T, VEC>(gx + (t + i) * a.grad_x_token + (unsigned)c, ox, part);
+                put<T, VEC>(gf + (t + i) * a.grad_forget_token + (unsigned)c, of, part);
+                if constexpr (GATED) put<T, VEC>(gg + (t + i) * a.grad_gate_token + (unsigned)c, og, part);
             }
         }
+        buf ^= 1;
     }
     if (k.bias) {
         __syncthreads();
 #pragma unroll
         for (int v = 0; v < VEC; v++) s_run[0][wave][v][lane].x = sum[v];
         __syncthreads();
-        if (wave == 0 && on) {
+        if (wave == 0) {
             Floats<VEC> total{};
 #pragma unroll
             for (int w = 0; w < kNW; w++)
 #pragma unroll
                 for (int v = 0; v < VEC; v++) total.v[v] += s_run[0][w][v][lane].x;
-            store_pack<float, VEC>(k.bias + item * (long long)a.channels + c, total);
+            put<float, VEC>(k.bias + item * (long long)a.channels + c, total, own);
         }
     }
-    if (on && wave == 0 && grad_state && p.chunk == 0) store_pack<float, VEC>(grad_state, carry);
+    if (wave == 0 && grad_state && p.chunk == 0) put<float, VEC>(grad_state, carry, own);
 }
 
 // Sums of `items` rows of partial sums, in a fixed order.
@@ -550,7 +646,7 @@ __global__ __launch_bounds__(kBlock) void rec_token_kernel(const gated_recurrenc
 #pragma unroll
     for (int v = 0; v < VEC; v++) {
         float keep, take;
-        gates(to_f32(z.v[v]) + bias.v[v], keep, take);
+        gates(to_f32(z.v[v]), -kLog2e * bias.v[v], keep, take);
         h.v[v] = fmaf(keep, h.v[v], to_f32(x.v[v]) * (a.coupled ? take : 1.0f));
         y.v[v] = round_fp32<T>(a.gate ? h.v[v] * activate_c<CONV2D_ACT_SILU>(to_f32(gate.v[v]), 0.0f) : h.v[v]);
     }
@@ -565,52 +661,45 @@ template <typename T, int VEC> hipError_t launch_token(const gated_recurrence_ar
 
 // ---------------------------------------------------------------------------- host
 
-struct Reach {
-    const void *p;
-    long long batch, token;
+// Channels of a lane: four bytes of a row, or one channel alone.
+template <typename Args> int vec_of(const Args &a) { return a.dtype == CONV2D_DTYPE_F32 || a.channels == 1 ? 1 : 2; }
+
+// What a call costs whole and split, in us: fixed, a tile of a sequence left whole (one after the
+// other), and the values moved for each that the call takes in or gives out, whole and split.
+struct Costs {
+    double fixed_whole, fixed_split, tile_us;
+    int moved_whole, moved_split;
 };
+// Measured, bf16, us whole / split into some 512 and 1024 workgroups; more chunks fill the card, but each
+// reads the records before it:
+//   sequences x tokens x channels   prompt             gradient
+//   1 x 128 x 1024                   7.5 /   9.6       24 /  18
+//   1 x 256 x 1024                  11.8 /   9.7       40 /  19
+//   1 x 4096 x 1024                  138 /  14.8       370 /  28, 35
+//   32 x 512 x 2048                   45 /  47, 66     138 / 137, 164
+//   8 x 4096 x 2048                  170 / 148, 165    513 / 323, 340
+//   16 x 2048 x 4096, ragged         274 / 344, 310    655 / 672, 659
+//   1 x 65536 x 1024                2520 / 158, 163   7030 / 334, 356
+constexpr Costs kPrompt{3.0, 9.0, 2.2, 4, 6}, kGradient{8.0, 17.0, 5.8, 9, 11};
+constexpr int kWorkgroups = 512;
 
-// Whether groups of `vec` channels of every row stand at whole multiples of their size.
-bool grouped(int vec, int eb, int channels, bool batches, std::initializer_list<Reach> rows, std::initializer_list<const float *> floats) {
-    if (channels % vec) return false;
-    for (const Reach &r : rows)
-        if (r.p && ((uintptr_t)r.p % (vec * eb) || r.token % vec || (batches && r.batch % vec))) return false;
-    for (const float *p : floats)
-        if ((uintptr_t)p % (4 * vec)) return false;
-    return true;
-}
-
-int vec_of(const gated_recurrence_args &a) {
-    const bool batches = !a.offsets;
-    const int vec = a.dtype == CONV2D_DTYPE_F32 ? 1 : 2;
-    return grouped(vec, 4 / vec, a.channels, batches,
-                   {{a.x, a.x_batch, a.x_token}, {a.forget, a.forget_batch, a.forget_token}, {a.gate, a.gate_batch, a.gate_token},
-                    {a.y, a.y_batch, a.y_token}},
-                   {a.forget_bias, a.state}) ? vec : 1;
-}
-
-int vec_of(const gated_recurrence_backward_args &a) {
-    const bool batches = !a.offsets;
-    const int vec = a.dtype == CONV2D_DTYPE_F32 ? 1 : 2;
-    return grouped(vec, 4 / vec, a.channels, batches,
-                   {{a.grad, a.grad_batch, a.grad_token}, {a.x, a.x_batch, a.x_token}, {a.forget, a.forget_batch, a.forget_token},
-                    {a.gate, a.gate_batch, a.gate_token}, {a.grad_x, a.grad_x_batch, a.grad_x_token},
-                    {a.grad_forget, a.grad_forget_batch, a.grad_forget_token}, {a.grad_gate, a.grad_gate_batch, a.grad_gate_token}},
-                   {a.forget_bias, a.state, a.grad_state}) ? vec : 1;
-}
-
-// Chunks for some 1024 workgroups. *longest: a bound of the tokens of the longest sequence.
-template <typename Args> RecCut cut(const Args &a, int vec, bool split) {
+// How a call is cut. A sequence left whole is walked by one workgroup for each 64 VEC channels, so its
+// length is a time; a split one is read twice.
+template <typename Args> RecCut cut(const Args &a, int vec, const Costs &costs, bool may_split) {
     RecCut k{};
     k.cblocks = (a.channels + 64 * vec - 1) / (64 * vec);
     const long long total = a.offsets ? a.tokens : a.tokens * a.nseq;
     long long longest = a.offsets ? (a.longest ? a.longest : 2 * (total / std::max(a.nseq, 1))) : a.tokens;
     if (longest > a.tokens) longest = a.tokens;
     k.run = kWhole;
-    if (split) {
-        const long long run = (total * k.cblocks / 1024 + kTile - 1) / kTile * kTile;
-        const long long least = 2 * kTile;
-        if (std::max(run, least) < longest) k.run = (int)std::max(run, least);
+    // us to move one value of each token and channel at 4.7 TB/s
+    const double value_us = (double)total * a.channels * dtype_bytes(a.dtype) / 4.7e6;
+    // ragged sequences and waits for other workgroups' loads make a walk longer than its tiles alone
+    const double walk = 1.3 * costs.tile_us * (double)((longest + kTile - 1) / kTile);
+    const double whole = costs.fixed_whole + std::max(walk, costs.moved_whole * value_us);
+    if (may_split && whole > costs.fixed_split + costs.moved_split * value_us) {
+        const long long run = total * k.cblocks / kWorkgroups / kTile * kTile + kTile;
+        if (run < longest) k.run = (int)run;
     }
     k.chunks = a.offsets ? 0 : (int)std::max((a.tokens + k.run - 1) / k.run, 1ll);
     k.items = a.offsets ? (int)(a.tokens / k.run + a.nseq) : k.chunks * a.nseq;
@@ -621,20 +710,32 @@ size_t record_bytes(const RecCut &k, int fields, int channels) {
     return k.run < kWhole ? ((size_t)k.items * fields * channels * 4 + 255) / 256 * 256 : 0;
 }
 
+// Calls f with the two as integral constants.
+template <typename F> hipError_t by_form(bool first, bool gated, F f) {
+    if (first) return gated ? f(std::true_type{}, std::true_type{}) : f(std::true_type{}, std::false_type{});
+    return gated ? f(std::false_type{}, std::true_type{}) : f(std::false_type{}, std::false_type{});
+}
+
 template <typename T, int VEC> hipError_t launch_prompt(const gated_recurrence_args &a, const RecCut &k, hipStream_t st) {
     const long long blocks = (long long)k.items * k.cblocks;
-    if (k.rec) {
-        const hipError_t e = launch_blocks(rec_prompt_kernel<T, VEC, true>, blocks, 64 * kNW, st, a, k);
-        if (e != hipSuccess) return e;
-    }
-    return launch_blocks(rec_prompt_kernel<T, VEC, false>, blocks, 64 * kNW, st, a, k);
+    return by_form(a.coupled, a.gate, [&](auto coupled, auto gated) {
+        constexpr bool C = decltype(coupled)::value, G = decltype(gated)::value;
+        hipError_t e = hipSuccess;
+        if (k.rec) e = launch_blocks(rec_first_kernel<T, VEC, C>, blocks, 64 * kNW, st, a, k);
+        return e != hipSuccess ? e : launch_blocks(rec_prompt_kernel<T, VEC, C, G>, blocks, 64 * kNW, st, a, k);
+    });
 }
 
 template <typename T, int VEC> hipError_t launch_back(const gated_recurrence_backward_args &a, const RecCut &k, hipStream_t st) {
     const long long blocks = (long long)k.items * k.cblocks;
     hipError_t e = hipSuccess;
-    if (blocks) e = launch_blocks(rec_back_first_kernel<T, VEC>, blocks, 64 * kNW, st, a, k);
-    if (blocks && e == hipSuccess) e = launch_blocks(rec_back_kernel<T, VEC>, blocks, 64 * kNW, st, a, k);
+    if (blocks)
+        e = by_form(a.channels % (64 * VEC) == 0, a.gate, [&](auto whole, auto gated) {
+            constexpr bool W = decltype(whole)::value, G = decltype(gated)::value;
+            const hipError_t e1 = k.rec ? launch_blocks(rec_back_first_kernel<T, VEC, W, G, true>, blocks, 64 * kNW, st, a, k)
+                                        : launch_blocks(rec_back_first_kernel<T, VEC, W, false, false>, blocks, 64 * kNW, st, a, k);
+            return e1 != hipSuccess ? e1 : launch_blocks(rec_back_kernel<T, VEC, W, G>, blocks, 64 * kNW, st, a, k);
+        });
     if (e == hipSuccess && a.grad_forget_bias)
         e = launch_blocks(rec_bias_kernel, (a.channels + 63) / 64, 1024, st, k.bias, a.grad_forget_bias, k.items, a.channels);
     return e;
@@ -647,7 +748,7 @@ struct BackLayout {
 
 BackLayout back_layout(const gated_recurrence_backward_args &a) {
     BackLayout l{};
-    l.k = cut(a, vec_of(a), true);
+    l.k = cut(a, vec_of(a), kGradient, true);
     l.rec = record_bytes(l.k, 3, a.channels);
     const long long tiles = a.offsets ? a.tokens / kTile + a.nseq : (a.tokens + kTile - 1) / kTile * a.nseq;
     l.tile = ((size_t)tiles * 2 * a.channels * 4 + 255) / 256 * 256;
@@ -658,16 +759,16 @@ BackLayout back_layout(const gated_recurrence_backward_args &a) {
 
 }  // namespace
 
-size_t recurrence_workspace(const gated_recurrence_args &a) { return record_bytes(cut(a, vec_of(a), true), 2, a.channels); }
+size_t recurrence_workspace(const gated_recurrence_args &a) { return record_bytes(cut(a, vec_of(a), kPrompt, true), 2, a.channels); }
 
 hipError_t launch_recurrence(const gated_recurrence_args &a, void *ws, size_t ws_bytes, hipStream_t st) {
     const int vec = vec_of(a);
-    RecCut k = cut(a, vec, true);
+    RecCut k = cut(a, vec, kPrompt, true);
     const size_t want = record_bytes(k, 2, a.channels);
     if (want && ws && want <= ws_bytes)
         k.rec = static_cast<float *>(ws);
     else
-        k = cut(a, vec, false);
+        k = cut(a, vec, kPrompt, false);
     if (a.dtype == CONV2D_DTYPE_F32) return launch_prompt<float, 1>(a, k, st);
     if (a.dtype == CONV2D_DTYPE_BF16) return vec == 2 ? launch_prompt<bf16, 2>(a, k, st) : launch_prompt<bf16, 1>(a, k, st);
     return vec == 2 ? launch_prompt<f16, 2>(a, k, st) : launch_prompt<f16, 1>(a, k, st);

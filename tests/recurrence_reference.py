@@ -1,9 +1,10 @@
 """The gated linear recurrence and its gradient from their definitions in 64 bits, token by token on the CPU, with
 bounds on the error a 32-bit evaluation may have.
 
-U32 = 2^-24 is the error of one 32-bit rounding. A gate sigmoid(z) of a sum z has, relatively, the errors of the sum and
-of exp's argument, three roundings of |z| times the slope of its logarithm, and six more (exp2, the sum, the reciprocal
-as two each). ``m`` bounds the sizes of the terms that make up a state or a carried gradient, which any order of joining
+U32 = 2^-24 is the error of one 32-bit rounding. The argument of a gate's exp2 is -log2(e) v + (-log2(e) bias), where
+the rounded constant is off by half a rounding, the second product by one more, and the sum by one: in z = v + bias
+that is U32 (|v| / 2 + 3 |bias| / 2 + |z|). exp2 adds two, relatively; the gate's logarithm has the slope of the other
+gate in it. The sum 1 + t and the reciprocal make three, the product for the other gate one more. ``m`` bounds the sizes of the terms that make up a state or a carried gradient, which any order of joining
 runs of tokens adds up; four roundings a token cover the products and sums of such an order.
 """
 import torch
@@ -17,10 +18,14 @@ def stored(y, error, dtype):
     return _rounded(y, error, dtype) if dtype in U else error
 
 
-def _gate(z):
-    """sigmoid, one minus it, and their relative errors."""
+def _gate(v, bias=None):
+    """sigmoid of the sum, one minus it, and their relative errors."""
+    b = torch.zeros(v.shape[-1], dtype=torch.float64) if bias is None else bias.double()
+    v = v.double()
+    z = v + b
     f, k = torch.sigmoid(z), torch.sigmoid(-z)
-    return f, k, U32 * (3 * z.abs() * k + 6), U32 * (3 * z.abs() * f + 6)
+    arg = v.abs() / 2 + 1.5 * b.abs() + z.abs() + 2
+    return f, k, U32 * (arg * k + 3) * 1.001, U32 * (arg * f + 4) * 1.001
 
 
 def _start(state, slots, i, d, fresh=False):
@@ -34,7 +39,7 @@ def forward(x, forget, gate, bias, coupled, state, slots, lengths, fresh=False):
     before it (for the gradient)."""
     tokens, d = x.shape
     xd = x.double()
-    f, k, rf, rk = _gate(forget.double() + (0 if bias is None else bias.double()))
+    f, k, rf, rk = _gate(forget, bias)
     b = k * xd if coupled else xd
     rb = (rk if coupled else 0 * rk) + 2 * U32
     new = None if state is None else state.double().clone()
@@ -68,7 +73,7 @@ def backward(grad, x, forget, gate, bias, coupled, state, grad_state, slots, len
     tokens, d = x.shape
     h, m, e, hb, mb, eb = forward(x, forget, gate, bias, coupled, state, slots, lengths)[4]
     xd, ed = x.double(), grad.double()
-    f, k, rf, rk = _gate(forget.double() + (0 if bias is None else bias.double()))
+    f, k, rf, rk = _gate(forget, bias)
     part, part_err = ed, torch.zeros_like(ed)
     dgate = dgate_err = None
     if gate is not None:

@@ -132,8 +132,8 @@ def test_workspace_sizes():
     assert _rec(size=True, **one) > 0
     assert _rec(size=True, nseq=0) == 0
     with_bias, without = _back(), _back(grad_forget_bias=0)
-    assert with_bias - without == 2 * D * 4
-    assert without >= 2 * 2 * 2 * D * 4  # two tiles of each of two sequences
+    assert with_bias - without >= 2 * D * 4  # a sum for each chunk
+    assert without >= 2 * 2 * 2 * D * 4  # two numbers for each of two tiles of two sequences
     c2d._load().conv2d_set_workspace(None, 0)
     assert _back(size=False) == c2d.EUNSUPPORTED
     assert "needs a workspace" in c2d.last_error()
