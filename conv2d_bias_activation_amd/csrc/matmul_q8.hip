@@ -249,11 +249,19 @@ struct Q8Args {
     int act, before;
 };
 
-// sum * sx * sw, the smaller scale first: nothing overflows or loses bits on the way that the
-// product itself does not (scales of quantized rows are normal numbers).
-__device__ __forceinline__ float scaled(int sum, float a, float b) {
+// sum * a * b + bias for the scales a and b. Scales of ordinary sizes are multiplied first; of others the
+// smaller one is applied first, so that nothing overflows or loses bits on the way that the
+// product itself does not (scales of quantized rows are normal numbers). Every kernel does the same.
+__device__ __forceinline__ bool ordinary(float a) { return fabsf(a) >= 0x1p-60f && fabsf(a) <= 0x1p60f; }
+__device__ __forceinline__ float affine(int sum, float a, float b, float bias) {
+    if (ordinary(a) && ordinary(b)) return fmaf((float)sum, a * b, bias);
     const bool less = fabsf(a) < fabsf(b);
-    return (float)sum * (less ? a : b) * (less ? b : a);
+    return (float)sum * (less ? a : b) * (less ? b : a) + bias;
+}
+
+// What the epilogue of conv2d_fused does behind the bias.
+__device__ __forceinline__ float behind_bias(float v, float alpha, float r, bool has_res, int act, bool before) {
+    return epilogue(v, 0.0f, alpha, r, has_res, act, before);
 }
 
 // A few rows: a workgroup computes 16 NT outputs of 16 MT rows, straight from memory; its W waves
@@ -322,7 +330,7 @@ __global__ __launch_bounds__(64 * W) void q8_few_kernel(const Q8Args a, int nblo
         int sum = 0;
 #pragma unroll
         for (int v = 0; v < W; v++) sum += s_sum[v][t][l][r];
-        const float v = epilogue(scaled(sum, sx[j], sw[j]), bias[j], alpha[j], res[j], a.residual != nullptr, a.act, a.before != 0);
+        const float v = behind_bias(affine(sum, sx[j], sw[j], bias[j]), alpha[j], res[j], a.residual != nullptr, a.act, a.before != 0);
         static_cast<T *>(a.y)[row[j] * a.y_row + o[j]] = round_fp32<T>(v);
     }
 }
@@ -412,7 +420,7 @@ __global__ __launch_bounds__(64 * kDirectWaves) void q8_direct_kernel(const Q8Ar
     int sum = 0;
 #pragma unroll
     for (int i = 0; i < W; i++) sum += s_sum[i][threadIdx.x / 16 % NT][row][threadIdx.x % 16];
-    const float f = epilogue(scaled(sum, sx, sw), bias, alpha, res, a.residual != nullptr, a.act, a.before != 0);
+    const float f = behind_bias(affine(sum, sx, sw, bias), alpha, res, a.residual != nullptr, a.act, a.before != 0);
     static_cast<T *>(a.y)[row * a.y_row + o] = round_fp32<T>(f);
 }
 
@@ -597,6 +605,9 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(const Q8Args a, i
     const T *res = static_cast<const T *>(a.residual);
     T *y = static_cast<T *>(a.y);
     const bool whole = o0 + VE <= a.outs;  // rows need not be aligned
+    bool plain = true;
+#pragma unroll
+    for (int e = 0; e < VE; e++) plain &= ordinary(sw[e]);
     auto finish_rows = [&](int row0, auto act) {
 #pragma unroll 2
         for (int p = 0; p < 32 / RP; p++) {
@@ -614,14 +625,21 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(const Q8Args a, i
                 }
             }
             const int *q = slice + (p * RP + lane / LPR) * LD + lane % LPR * VE;
+            float v[VE];
+            if (plain && ordinary(sx)) {
+#pragma unroll
+                for (int e = 0; e < VE; e++) v[e] = fmaf((float)q[e], sx * sw[e], bias[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VE; e++) v[e] = affine(q[e], sx, sw[e], bias[e]);
+            }
 #pragma unroll
             for (int e = 0; e < VE; e++) {
-                float v = scaled(q[e], sx, sw[e]) + bias[e];
                 const float add = to_f32(r.v[e]);
-                if (res && a.before) v += add;
-                v = activate_c<decltype(act)::value>(v, alpha[e]);
-                if (res && !a.before) v += add;
-                out.v[e] = round_fp32<T>(v);
+                if (res && a.before) v[e] += add;
+                v[e] = activate_c<decltype(act)::value>(v[e], alpha[e]);
+                if (res && !a.before) v[e] += add;
+                out.v[e] = round_fp32<T>(v[e]);
             }
             if (whole) {
                 __builtin_memcpy(y + row * a.y_row + o0, &out, sizeof out);
