@@ -661,27 +661,31 @@ template <typename T, int VEC> hipError_t launch_token(const gated_recurrence_ar
 
 // ---------------------------------------------------------------------------- host
 
-// Channels of a lane: four bytes of a row, or one channel alone.
-template <typename Args> int vec_of(const Args &a) { return a.dtype == CONV2D_DTYPE_F32 || a.channels == 1 ? 1 : 2; }
-
 // What a call costs whole and split, in us: fixed, a tile of a sequence left whole (one after the
 // other), and the values moved for each that the call takes in or gives out, whole and split.
 struct Costs {
     double fixed_whole, fixed_split, tile_us;
     int moved_whole, moved_split;
 };
-// Measured, bf16, us whole / split into some 512 and 1024 workgroups; more chunks fill the card, but each
-// reads the records before it:
+// Measured, bf16, us whole / split:
 //   sequences x tokens x channels   prompt             gradient
-//   1 x 128 x 1024                   7.5 /   9.6       24 /  18
 //   1 x 256 x 1024                  11.8 /   9.7       40 /  19
-//   1 x 4096 x 1024                  138 /  14.8       370 /  28, 35
-//   32 x 512 x 2048                   45 /  47, 66     138 / 137, 164
-//   8 x 4096 x 2048                  170 / 148, 165    513 / 323, 340
-//   16 x 2048 x 4096, ragged         274 / 344, 310    655 / 672, 659
-//   1 x 65536 x 1024                2520 / 158, 163   7030 / 334, 356
+//   1 x 4096 x 1024                  138 /  14.8       370 /  28
+//   32 x 512 x 2048                   45 /  47         138 / 137
+//   8 x 4096 x 2048                  170 / 133         513 / 310
+//   16 x 2048 x 4096, ragged         274 / 310         590 / 659
+//   1 x 65536 x 1024                2520 / 148        7030 / 307
 constexpr Costs kPrompt{3.0, 9.0, 2.2, 4, 6}, kGradient{8.0, 17.0, 5.8, 9, 11};
-constexpr int kWorkgroups = 512;
+
+// Workgroups of a split call. One for each CU, and no more, where the sequences are as long as each other: the
+// gradient's hold a CU's registers alone, and a second round of a few costs as much as a full
+// one. Ragged ones even out over three. Into 256, 384, 512, 768, 1024 workgroups, us:
+//   1 x 65536 x 1024, prompt              148, 175, 150, 153, 153
+//   1 x 65536 x 1024, gradient            307, 379, 316, 326, 346
+//   1 x 20000 x 256, gradient             36.8, 53.8, 53.5, 72.9, 72.7
+//   8 x 1000 x 2048, ragged, prompt       54.2, 44.5, 44.6, 38.6, 42.3
+//   8 x 1000 x 2048, ragged, gradient     100, 94.0, 91.9, 84.5, 95.8
+constexpr int kWorkgroups = 256, kRaggedWorkgroups = 768;
 
 // How a call is cut. A sequence left whole is walked by one workgroup for each 64 VEC channels, so its
 // length is a time; a split one is read twice.
@@ -698,12 +702,22 @@ template <typename Args> RecCut cut(const Args &a, int vec, const Costs &costs, 
     const double walk = 1.3 * costs.tile_us * (double)((longest + kTile - 1) / kTile);
     const double whole = costs.fixed_whole + std::max(walk, costs.moved_whole * value_us);
     if (may_split && whole > costs.fixed_split + costs.moved_split * value_us) {
-        const long long run = total * k.cblocks / kWorkgroups / kTile * kTile + kTile;
+        const long long parts = a.offsets && a.nseq > 1 ? kRaggedWorkgroups : kWorkgroups;
+        const long long run = std::max((total * k.cblocks + parts * kTile - 1) / (parts * kTile), 1ll) * kTile;
         if (run < longest) k.run = (int)run;
     }
     k.chunks = a.offsets ? 0 : (int)std::max((a.tokens + k.run - 1) / k.run, 1ll);
     k.items = a.offsets ? (int)(a.tokens / k.run + a.nseq) : k.chunks * a.nseq;
     return k;
+}
+
+// The channels of a lane, and the cut of a call with them: two of 16 bits, four bytes of a row, but one
+// where tiles of two would not make a workgroup for each CU (us: 1 x 77 x 512 8.1 and 6.3, 1 x 1024 x 1024
+// 10.3 and 8.7, its gradient 18.2 and 14.7; 1 x 4096 x 1024 15.3 and 19.6).
+template <typename Args> RecCut plan(const Args &a, const Costs &costs, bool may_split, int *vec) {
+    const long long total = a.offsets ? a.tokens : a.tokens * a.nseq;
+    *vec = a.dtype == CONV2D_DTYPE_F32 || a.channels == 1 || total * ((a.channels + 127) / 128) < (long long)kWorkgroups * kTile ? 1 : 2;
+    return cut(a, *vec, costs, may_split);
 }
 
 size_t record_bytes(const RecCut &k, int fields, int channels) {
@@ -743,12 +757,13 @@ template <typename T, int VEC> hipError_t launch_back(const gated_recurrence_bac
 
 struct BackLayout {
     RecCut k;
+    int vec;
     size_t rec, tile, bias, bytes;
 };
 
 BackLayout back_layout(const gated_recurrence_backward_args &a) {
     BackLayout l{};
-    l.k = cut(a, vec_of(a), kGradient, true);
+    l.k = plan(a, kGradient, true, &l.vec);
     l.rec = record_bytes(l.k, 3, a.channels);
     const long long tiles = a.offsets ? a.tokens / kTile + a.nseq : (a.tokens + kTile - 1) / kTile * a.nseq;
     l.tile = ((size_t)tiles * 2 * a.channels * 4 + 255) / 256 * 256;
@@ -759,16 +774,19 @@ BackLayout back_layout(const gated_recurrence_backward_args &a) {
 
 }  // namespace
 
-size_t recurrence_workspace(const gated_recurrence_args &a) { return record_bytes(cut(a, vec_of(a), kPrompt, true), 2, a.channels); }
+size_t recurrence_workspace(const gated_recurrence_args &a) {
+    int vec;
+    return record_bytes(plan(a, kPrompt, true, &vec), 2, a.channels);
+}
 
 hipError_t launch_recurrence(const gated_recurrence_args &a, void *ws, size_t ws_bytes, hipStream_t st) {
-    const int vec = vec_of(a);
-    RecCut k = cut(a, vec, kPrompt, true);
+    int vec;
+    RecCut k = plan(a, kPrompt, true, &vec);
     const size_t want = record_bytes(k, 2, a.channels);
     if (want && ws && want <= ws_bytes)
         k.rec = static_cast<float *>(ws);
     else
-        k = cut(a, vec, kPrompt, false);
+        k = plan(a, kPrompt, false, &vec);
     if (a.dtype == CONV2D_DTYPE_F32) return launch_prompt<float, 1>(a, k, st);
     if (a.dtype == CONV2D_DTYPE_BF16) return vec == 2 ? launch_prompt<bf16, 2>(a, k, st) : launch_prompt<bf16, 1>(a, k, st);
     return vec == 2 ? launch_prompt<f16, 2>(a, k, st) : launch_prompt<f16, 1>(a, k, st);
@@ -792,7 +810,7 @@ hipError_t launch_recurrence_backward(const gated_recurrence_backward_args &a, v
     if (l.rec) l.k.rec = reinterpret_cast<float *>(p);
     l.k.tile = reinterpret_cast<float *>(p + l.rec);
     if (a.grad_forget_bias) l.k.bias = reinterpret_cast<float *>(p + l.rec + l.tile);
-    const int vec = vec_of(a);
+    const int vec = l.vec;
     if (a.dtype == CONV2D_DTYPE_F32) return launch_back<float, 1>(a, l.k, st);
     if (a.dtype == CONV2D_DTYPE_BF16) return vec == 2 ? launch_back<bf16, 2>(a, l.k, st) : launch_back<bf16, 1>(a, l.k, st);
     return vec == 2 ? launch_back<f16, 2>(a, l.k, st) : launch_back<f16, 1>(a, l.k, st);
