@@ -41,6 +41,7 @@ struct RecCut {
     int items;    // chunk numbers in all (find_run), or nseq * chunks
     int chunks;   // unpacked: chunks of a sequence
     int cblocks;  // blocks of 64 VEC channels
+    int ranked;   // whole packed sequences: how many stand side by side on the card, else 0
     float *rec;   // split sequences: records of the chunks, [item][fields][channels]
     float *tile;  // gradient: [tile number][2][channels]
     float *bias;  // gradient: sums of grad_forget, [item][channels]
@@ -79,6 +80,34 @@ template <typename Args> __device__ __forceinline__ bool place_of(const Args &a,
     p.last = p.r.len > 0 ? (p.r.len - 1) / k.run : 0;
     p.end = min(p.r.len, p.r.first + k.run);
     return true;
+}
+
+constexpr int kMaxRanked = 256;
+
+// The sequence at place `at` of whole packed ones. The first `side` of them have a CU each for every block
+// of channels, the next `side` share those CUs, and so on: the longest come first, and every other
+// row of `side` runs backwards, so that long ones share with short ones. In this order and in
+// that of their numbers, bf16, us: 16 ragged sequences of 32768 tokens x 4096 in all 238 and 276, 32 of
+// 32000 x 2048 123 and 154, 64 of 8192 x 2048 34 and 36; 200 of 28000 x 1024 61 and 54. key: room for
+// kMaxRanked.
+__device__ __forceinline__ int by_length(const int *offsets, int nseq, int tokens, int at, int side, uint64_t *key, int &found) {
+    for (int i = threadIdx.x; i < nseq; i += blockDim.x) {
+        const int len = clamped_offset(offsets, i + 1, tokens) - clamped_offset(offsets, i, tokens);
+        key[i] = (uint64_t)max(len, 0) << 32 | (uint32_t)(nseq - i);  // ties by number
+    }
+    __syncthreads();
+    const int row = at / side, first = row * side, last = min(first + side, nseq) - 1;
+    const int rank = row % 2 ? last - (at - first) : at;
+    for (int i = threadIdx.x; i < nseq; i += blockDim.x) {
+        const uint64_t mine = key[i];
+        int before = 0;
+        for (int j = 0; j < nseq; j++) before += key[j] > mine;
+        if (before == rank) found = i;
+    }
+    __syncthreads();
+    const int seq = __builtin_amdgcn_readfirstlane(found);
+    __syncthreads();  // the keys' room is free again
+    return seq;
 }
 
 template <typename T> __device__ __forceinline__ const T *rows(const void *p, const Place &w, long long batch, long long token) {
@@ -245,7 +274,10 @@ __global__ __launch_bounds__(64 * kNW, 4) void rec_prompt_kernel(const gated_rec
     __shared__ float2 s_run[2][kNW][VEC][64];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     // the second pass takes the chunks that the first read last first: they may still be cached
-    const int item = k.items - 1 - blockIdx.x / k.cblocks;
+    __shared__ int s_found;
+    const int place = blockIdx.x / k.cblocks;
+    const int item = k.ranked ? by_length(a.offsets, a.nseq, (int)a.tokens, place, k.ranked, reinterpret_cast<uint64_t *>(s_run), s_found)
+                              : k.items - 1 - place;
     const auto [c, own] = channels_of<VEC>(((int)(blockIdx.x % k.cblocks) * 64 + lane) * VEC, a.channels);
     Place p;
     if (!place_of(a, k, item, p)) return;
@@ -344,7 +376,9 @@ template <typename T, int VEC, bool WHOLE, bool GATED, bool SPLIT>
 __global__ __launch_bounds__(64 * kNW) void rec_back_first_kernel(const gated_recurrence_backward_args a, const RecCut k) {
     __shared__ float4 s_run[2][kNW][VEC][64];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int item = blockIdx.x / k.cblocks;
+    __shared__ int s_found;
+    int item = blockIdx.x / k.cblocks;
+    if (k.ranked) item = by_length(a.offsets, a.nseq, (int)a.tokens, item, k.ranked, reinterpret_cast<uint64_t *>(s_run), s_found);
     // WHOLE: the channels fill their blocks
     const auto [c, own] = channels_of<VEC>(((int)(blockIdx.x % k.cblocks) * 64 + lane) * VEC, a.channels);
     Place p;
@@ -454,7 +488,10 @@ template <typename T, int VEC, bool WHOLE, bool GATED>
 __global__ __launch_bounds__(64 * kNW) void rec_back_kernel(const gated_recurrence_backward_args a, const RecCut k) {
     __shared__ float4 s_run[2][kNW][VEC][64];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int item = k.items - 1 - blockIdx.x / k.cblocks;
+    __shared__ int s_found;
+    const int place = blockIdx.x / k.cblocks;
+    const int item = k.ranked ? by_length(a.offsets, a.nseq, (int)a.tokens, place, k.ranked, reinterpret_cast<uint64_t *>(s_run), s_found)
+                              : k.items - 1 - place;
     const auto [c, own] = channels_of<VEC>(((int)(blockIdx.x % k.cblocks) * 64 + lane) * VEC, a.channels);
     float sum[VEC];
 #pragma unroll
@@ -666,6 +703,7 @@ template <typename T, int VEC> hipError_t launch_token(const gated_recurrence_ar
 struct Costs {
     double fixed_whole, fixed_split, tile_us;
     int moved_whole, moved_split;
+    bool share;  // workgroups share CUs (the gradient's hold one each)
 };
 // Measured, bf16, us whole / split:
 //   sequences x tokens x channels   prompt             gradient
@@ -675,7 +713,7 @@ struct Costs {
 //   8 x 4096 x 2048                  170 / 133         513 / 310
 //   16 x 2048 x 4096, ragged         274 / 310         590 / 659
 //   1 x 65536 x 1024                2520 / 148        7030 / 307
-constexpr Costs kPrompt{3.0, 9.0, 2.2, 4, 6}, kGradient{8.0, 17.0, 5.8, 9, 11};
+constexpr Costs kPrompt{3.0, 9.0, 2.2, 4, 6, true}, kGradient{8.0, 17.0, 5.8, 9, 11, false};
 
 // Workgroups of a split call. One for each CU, and no more, where the sequences are as long as each other: the
 // gradient's hold a CU's registers alone, and a second round of a few costs as much as a full
@@ -708,6 +746,10 @@ template <typename Args> RecCut cut(const Args &a, int vec, const Costs &costs, 
     }
     k.chunks = a.offsets ? 0 : (int)std::max((a.tokens + k.run - 1) / k.run, 1ll);
     k.items = a.offsets ? (int)(a.tokens / k.run + a.nseq) : k.chunks * a.nseq;
+    // the order costs each workgroup a look at all lengths, which long sequences earn back
+    if (a.offsets && k.run == kWhole && k.items == a.nseq && a.nseq <= kMaxRanked && (long long)a.nseq * k.cblocks > kWorkgroups &&
+        a.tokens >= 2ll * a.nseq * a.nseq)
+        k.ranked = costs.share ? std::max(kWorkgroups / k.cblocks, 1) : kMaxRanked;
     return k;
 }
 
