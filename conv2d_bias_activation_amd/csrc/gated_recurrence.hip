@@ -783,7 +783,8 @@ template <typename T, int VEC> hipError_t launch_prompt(const gated_recurrence_a
 }
 
 template <typename T, int VEC> hipError_t launch_back(const gated_recurrence_backward_args &a, const RecCut &k, hipStream_t st) {
-    const long long blocks = (long long)k.items * k.cblocks;
+    const long long blocks = (long long)k.items * k.cblocks, bias_blocks = (a.channels + 63) / 64;
+    if (a.grad_forget_bias && bias_blocks > 0xffffffffll / 1024) return hipErrorInvalidConfiguration;  // before any launch
     hipError_t e = hipSuccess;
     if (blocks)
         e = by_form(a.channels % (64 * VEC) == 0, a.gate, [&](auto whole, auto gated) {
@@ -793,7 +794,7 @@ template <typename T, int VEC> hipError_t launch_back(const gated_recurrence_bac
             return e1 != hipSuccess ? e1 : launch_blocks(rec_back_kernel<T, VEC, W, G>, blocks, 64 * kNW, st, a, k);
         });
     if (e == hipSuccess && a.grad_forget_bias)
-        e = launch_blocks(rec_bias_kernel, (a.channels + 63) / 64, 1024, st, k.bias, a.grad_forget_bias, k.items, a.channels);
+        e = launch_blocks(rec_bias_kernel, bias_blocks, 1024, st, k.bias, a.grad_forget_bias, k.items, a.channels);
     return e;
 }
 

@@ -177,6 +177,33 @@ def test_gradients_as_slices_of_one_tensor():
         assert torch.equal(g, w)
 
 
+@pytest.mark.parametrize("lengths,rows,d", [([30, 0, 41], 100, 40), ([500, 1, 300], 900, 130)])
+def test_rows_behind_the_last_sequence_stay(lengths, rows, d):
+    """A padded packed batch: rows that no sequence covers are neither read into a result nor written."""
+    n = sum(lengths)
+    c = _case(n, "bf16", [rows], True, d, {"state": False})
+    kw = _kw(c, lengths, True, {})
+    args = [_on(c[k]) for k in ("grad", "x", "forget")]
+    for t in (*args, kw["gate"]):
+        t[n:] = float("nan")
+    cut = {**kw, "gate": kw["gate"][:n]}
+    outs = [torch.full((rows, d), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(4)]
+    c2d.gated_recurrence(args[1], args[2], out=outs[3], **kw)
+    got = c2d.gated_recurrence_backward(*args, out=tuple(outs[:3]), **kw)
+    want_y = c2d.gated_recurrence(args[1][:n], args[2][:n], workspace=False, **cut)
+    want = c2d.gated_recurrence_backward(*(t[:n] for t in args), **cut)
+    # the two calls may be cut differently, so they are compared with the definition
+    for o in outs:
+        assert (o[n:] == 7).all()
+    y, bound, *_ = rec.forward(c["x"][:n], c["forget"][:n], c["gate"][:n], c["bias"], True, None, None, lengths)
+    ref.close(outs[3][:n], y, bound, "padded")
+    ref.close(want_y, y, bound, "not padded")
+    grads = rec.backward(c["grad"][:n], c["x"][:n], c["forget"][:n], c["gate"][:n], c["bias"], True, None, None, None, lengths)
+    for g, w, (value, bound) in zip(got, want, grads):
+        ref.close(g[:n] if g.dim() == 2 else g, value, bound, "padded gradient")
+        ref.close(w, value, bound, "gradient")
+
+
 def test_offsets_past_32_bits():
     """Rows so far apart that an element's index passes 2^31, read and written in place."""
     d, n, pitch = 8, 300, 1 << 23

@@ -59,6 +59,12 @@ def test_too_large_is_unsupported(call, kw):
     assert call(**kw) == c2d.EUNSUPPORTED
 
 
+def test_too_many_threads_are_refused():
+    assert _rows(rows=1 << 27, in_features=64, x_row=64, packed=100 * G) == c2d.EUNSUPPORTED and "2^32" in c2d.last_error()
+    many = dict(x=0, x_packed=1 << 45, rows=1 << 20, out_features=1 << 20, in_features=64, y=1 << 50, y_row=1 << 20)
+    assert _matmul(**many) == c2d.EUNSUPPORTED and "2^32" in c2d.last_error()
+
+
 def test_sizes():
     n = ctypes.c_size_t(0)
     size = c2d._load().q8_packed_bytes

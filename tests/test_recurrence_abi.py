@@ -126,6 +126,26 @@ def test_too_large_is_unsupported(call, kw):
     assert call(**kw) == c2d.EUNSUPPORTED
 
 
+def _wide(channels, back, **kw):
+    rows = ("grad", "x", "forget", "grad_x", "grad_forget") if back else ("x", "forget", "y")
+    return dict(channels=channels, tokens=1, nseq=1, gate=0, state=0, state_rows=0, **({"grad_gate": 0, "grad_state": 0} if back else {}),
+                **{f"{t}_{k}": channels for t in rows for k in ("batch", "token")}, **kw)
+
+
+def test_too_many_threads_are_refused_before_any_launch():
+    lib = c2d._load()
+    assert _rec(**_wide(1 << 30, False, dtype=c2d.DTYPE_F32)) == c2d.EUNSUPPORTED and "2^32" in c2d.last_error()
+    assert _rec(step=True, **_wide(1 << 24, False, y=1 << 40) | dict(nseq=1 << 20, x_token=0, forget_token=0)) == c2d.EUNSUPPORTED
+    assert "2^32" in c2d.last_error()
+    lib.conv2d_set_workspace(100 * G, 1 << 45)
+    try:
+        # the gradient's own launches, and the bias gradient's alone
+        assert _back(size=False, **_wide(1 << 30, True, dtype=c2d.DTYPE_F32)) == c2d.EUNSUPPORTED and "2^32" in c2d.last_error()
+        assert _back(size=False, **_wide(1 << 28, True)) == c2d.EUNSUPPORTED and "2^32" in c2d.last_error()
+    finally:
+        lib.conv2d_set_workspace(None, 0)
+
+
 def test_workspace_sizes():
     assert _rec(size=True) == 0  # two short sequences: not split
     one = dict(nseq=1, tokens=20000)
