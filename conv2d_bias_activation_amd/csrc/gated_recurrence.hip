@@ -222,10 +222,12 @@ __global__ __launch_bounds__(64 * kNW) void rec_first_kernel(const gated_recurre
     float At[VEC], Bt[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; v++) At[v] = 1.0f, Bt[v] = 0.0f;
-    const int part = k.run / kNW, t0 = p.r.first + wave * part, t1 = t0 + part;
+    const int part = (k.run + kNW * kTW - 1) / (kNW * kTW) * kTW, t0 = p.r.first + wave * part, t1 = min(t0 + part, p.end);
     Pack<T, VEC> nx[kTW], nf[kTW];
-    fetch<T, VEC>(nf, forget, a.forget_token, t0, t1, c);
-    fetch<T, VEC>(nx, x, a.x_token, t0, t1, c);
+    if (t0 < t1) {
+        fetch<T, VEC>(nf, forget, a.forget_token, t0, t1, c);
+        fetch<T, VEC>(nx, x, a.x_token, t0, t1, c);
+    }
     for (int t = t0; t < t1; t += kTW) {
         float f[kTW][VEC], b[kTW][VEC];
 #pragma unroll
@@ -372,14 +374,13 @@ __global__ __launch_bounds__(64 * kNW, 4) void rec_prompt_kernel(const gated_rec
 
 // The first pass of the gradient walks forwards: it leaves, for each tile, the state before it as
 // an affine map of the state before the chunk, and, for split sequences, the chunks' records.
-template <typename T, int VEC, bool WHOLE, bool GATED, bool SPLIT>
+template <typename T, int VEC, bool GATED, bool SPLIT>
 __global__ __launch_bounds__(64 * kNW) void rec_back_first_kernel(const gated_recurrence_backward_args a, const RecCut k) {
     __shared__ float4 s_run[2][kNW][VEC][64];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     __shared__ int s_found;
     int item = blockIdx.x / k.cblocks;
     if (k.ranked) item = by_length(a.offsets, a.nseq, (int)a.tokens, item, k.ranked, reinterpret_cast<uint64_t *>(s_run), s_found);
-    // WHOLE: the channels fill their blocks
     const auto [c, own] = channels_of<VEC>(((int)(blockIdx.x % k.cblocks) * 64 + lane) * VEC, a.channels);
     Place p;
     if (!place_of(a, k, item, p)) return;
@@ -483,7 +484,8 @@ __global__ __launch_bounds__(64 * kNW) void rec_back_first_kernel(const gated_re
     put<float, VEC>(q + kD * (long long)a.channels, E, own);
 }
 
-// The second pass walks backwards over the tiles and writes the gradients.
+// The second pass walks backwards over the tiles and writes the gradients. WHOLE: the channels fill
+// their blocks.
 template <typename T, int VEC, bool WHOLE, bool GATED>
 __global__ __launch_bounds__(64 * kNW) void rec_back_kernel(const gated_recurrence_backward_args a, const RecCut k) {
     __shared__ float4 s_run[2][kNW][VEC][64];
@@ -699,55 +701,85 @@ template <typename T, int VEC> hipError_t launch_token(const gated_recurrence_ar
 // ---------------------------------------------------------------------------- host
 
 // What a call costs whole and split, in us: fixed, a tile of a sequence left whole (one after the
-// other), and the values moved for each that the call takes in or gives out, whole and split.
+// other), and the values moved for each that the call takes in or gives out, whole and split (a second
+// pass finds a few of its values cached).
 struct Costs {
-    double fixed_whole, fixed_split, tile_us;
-    int moved_whole, moved_split;
+    double fixed_whole, fixed_split, tile_us, moved_whole, moved_split;
     bool share;  // workgroups share CUs (the gradient's hold one each)
 };
 // Measured, bf16, us whole / split:
 //   sequences x tokens x channels   prompt             gradient
 //   1 x 256 x 1024                  11.8 /   9.7       40 /  19
-//   1 x 4096 x 1024                  138 /  14.8       370 /  28
+//   1 x 4096 x 1024                  147 /  17         368 /  31
 //   32 x 512 x 2048                   45 /  47         138 / 137
-//   8 x 4096 x 2048                  170 / 133         513 / 310
+//   12 x 1000 x 1280                  44 /  38         115 /  83
+//   8 x 4096 x 2048                  170 / 133         513 / 305
+//   8 x 4096 x 2176                  178 / 157         460 / 343
+//   16 x 2048 x 2176                 159 / 152         410 / 350
 //   16 x 2048 x 4096, ragged         274 / 310         590 / 659
 //   1 x 65536 x 1024                2520 / 148        7030 / 307
-constexpr Costs kPrompt{3.0, 9.0, 2.2, 4, 6, true}, kGradient{8.0, 17.0, 5.8, 9, 11, false};
+constexpr Costs kPrompt{3.0, 9.0, 2.2, 4.0, 4.7, true}, kGradient{8.0, 17.0, 5.8, 9.0, 10.3, false};
 
-// Workgroups of a split call. One for each CU, and no more, where the sequences are as long as each other: the
-// gradient's hold a CU's registers alone, and a second round of a few costs as much as a full
-// one. Ragged ones even out over three. Into 256, 384, 512, 768, 1024 workgroups, us:
-//   1 x 65536 x 1024, prompt              148, 175, 150, 153, 153
-//   1 x 65536 x 1024, gradient            307, 379, 316, 326, 346
-//   1 x 20000 x 256, gradient             36.8, 53.8, 53.5, 72.9, 72.7
-//   8 x 1000 x 2048, ragged, prompt       54.2, 44.5, 44.6, 38.6, 42.3
-//   8 x 1000 x 2048, ragged, gradient     100, 94.0, 91.9, 84.5, 95.8
-constexpr int kWorkgroups = 256, kRaggedWorkgroups = 768;
+constexpr int kWorkgroups = 256;        // that the card runs at full speed side by side: one for each CU
+constexpr int kRaggedWorkgroups = 768;  // of a split call whose sequences are not as long as each other, which evens them out
+// (8 x 1000 x 2048, ragged, into 256, 384, 512, 768, 1024 workgroups, us: prompt 54.2, 44.5, 44.6, 38.6,
+// 42.3, gradient 100, 94.0, 91.9, 84.5, 95.8)
+
+// How long that many equal workgroups take, in the time of one among kWorkgroups: those of a last
+// round that does not fill the card are faster, but not by as much as they are fewer.
+double rounds(long long groups) {
+    if (groups <= kWorkgroups) return 1.0;
+    const double rest = (double)(groups % kWorkgroups) / kWorkgroups;
+    return (double)(groups / kWorkgroups) + (rest > 0.0 ? 0.6 + 0.4 * rest : 0.0);
+}
+
+// The tiles of a chunk that equal sequences of `tiles` tiles, each in `wide` blocks of channels, are
+// best split into: nearly whole rounds of workgroups, few chunks. By its factor over a full card's time the call
+// takes longer. Into 2, 3, 4, 5, 6 chunks a sequence, us:
+//   8 x 4096 x 2176 (272 to 816 workgroups)     prompt 187, 159, 169, 157, 161   gradient 483, 365, 401, 346, 368
+//   16 x 4096 x 1024 (256 to 768)                      133, 166, 138, 159, 145            308, 378, 303, 348, 321
+//   3 x 2048 x 4096 (192 to 576)                        63,  62,  58,  55,  60            135, 158, 131, 121, 125
+long long best_run(long long tiles, long long wide, double *factor) {
+    constexpr double kStart = 0.35;  // tiles' time that a workgroup takes to start
+    const double full = (double)(tiles * wide) / kWorkgroups;
+    long long run = tiles;
+    double least = 0.0;
+    for (int full_rounds = 1; full_rounds <= 8; full_rounds++) {
+        const long long c = std::min(std::max(full_rounds * kWorkgroups / wide, 2ll), tiles);
+        const long long r = (tiles + c - 1) / c, groups = (tiles + r - 1) / r * wide;
+        const double time = rounds(groups) * (double)r + kStart * (double)((groups + kWorkgroups - 1) / kWorkgroups);
+        if (full_rounds == 1 || time < least) run = r, least = time;
+    }
+    *factor = least / (full + kStart);
+    return run;
+}
 
 // How a call is cut. A sequence left whole is walked by one workgroup for each 64 VEC channels, so its
 // length is a time; a split one is read twice.
 template <typename Args> RecCut cut(const Args &a, int vec, const Costs &costs, bool may_split) {
     RecCut k{};
     k.cblocks = (a.channels + 64 * vec - 1) / (64 * vec);
+    const bool ragged = a.offsets && a.nseq > 1;
     const long long total = a.offsets ? a.tokens : a.tokens * a.nseq;
     long long longest = a.offsets ? (a.longest ? a.longest : 2 * (total / std::max(a.nseq, 1))) : a.tokens;
     if (longest > a.tokens) longest = a.tokens;
+    const long long tiles = (longest + kTile - 1) / kTile, wide = (long long)a.nseq * k.cblocks;
     k.run = kWhole;
     // us to move one value of each token and channel at 4.7 TB/s
     const double value_us = (double)total * a.channels * dtype_bytes(a.dtype) / 4.7e6;
     // ragged sequences and waits for other workgroups' loads make a walk longer than its tiles alone
-    const double walk = 1.3 * costs.tile_us * (double)((longest + kTile - 1) / kTile);
+    const double walk = 1.3 * costs.tile_us * (double)tiles * (ragged ? 1.0 : rounds(wide));
     const double whole = costs.fixed_whole + std::max(walk, costs.moved_whole * value_us);
-    if (may_split && whole > costs.fixed_split + costs.moved_split * value_us) {
-        const long long parts = a.offsets && a.nseq > 1 ? kRaggedWorkgroups : kWorkgroups;
-        const long long run = std::max((total * k.cblocks + parts * kTile - 1) / (parts * kTile), 1ll) * kTile;
-        if (run < longest) k.run = (int)run;
+    if (may_split && wide && whole > costs.fixed_split + costs.moved_split * value_us) {
+        double factor = 1.0;
+        const long long run = ragged ? std::max((total * k.cblocks + kRaggedWorkgroups * kTile - 1) / (kRaggedWorkgroups * kTile), 1ll)
+                                     : best_run(tiles, wide, &factor);
+        if (run < tiles && whole > costs.fixed_split + costs.moved_split * value_us * factor) k.run = (int)(run * kTile);
     }
     k.chunks = a.offsets ? 0 : (int)std::max((a.tokens + k.run - 1) / k.run, 1ll);
     k.items = a.offsets ? (int)(a.tokens / k.run + a.nseq) : k.chunks * a.nseq;
     // the order costs each workgroup a look at all lengths, which long sequences earn back
-    if (a.offsets && k.run == kWhole && k.items == a.nseq && a.nseq <= kMaxRanked && (long long)a.nseq * k.cblocks > kWorkgroups &&
+    if (a.offsets && k.run == kWhole && k.items == a.nseq && a.nseq <= kMaxRanked && wide > kWorkgroups &&
         a.tokens >= 2ll * a.nseq * a.nseq)
         k.ranked = costs.share ? std::max(kWorkgroups / k.cblocks, 1) : kMaxRanked;
     return k;
@@ -789,8 +821,8 @@ template <typename T, int VEC> hipError_t launch_back(const gated_recurrence_bac
     if (blocks)
         e = by_form(a.channels % (64 * VEC) == 0, a.gate, [&](auto whole, auto gated) {
             constexpr bool W = decltype(whole)::value, G = decltype(gated)::value;
-            const hipError_t e1 = k.rec ? launch_blocks(rec_back_first_kernel<T, VEC, W, G, true>, blocks, 64 * kNW, st, a, k)
-                                        : launch_blocks(rec_back_first_kernel<T, VEC, W, false, false>, blocks, 64 * kNW, st, a, k);
+            const hipError_t e1 = k.rec ? launch_blocks(rec_back_first_kernel<T, VEC, G, true>, blocks, 64 * kNW, st, a, k)
+                                        : launch_blocks(rec_back_first_kernel<T, VEC, false, false>, blocks, 64 * kNW, st, a, k);
             return e1 != hipSuccess ? e1 : launch_blocks(rec_back_kernel<T, VEC, W, G>, blocks, 64 * kNW, st, a, k);
         });
     if (e == hipSuccess && a.grad_forget_bias)

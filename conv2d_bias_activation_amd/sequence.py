@@ -1,6 +1,7 @@
-"""Sequence operators of the library (include/sequence_ops.h): the short causal convolution
-and the selective state space scan, for prompts and for single tokens, and products of a few
-token rows with 4-bit weights.
+"""Sequence operators of the library (include/sequence_ops.h): the short causal convolution,
+the selective state space scan and the gated linear recurrence, for prompts and for single
+tokens, the recurrence's gradient, products of a few token rows with 4-bit weights, and products
+of any number of them in 8-bit integers.
 
 As in the rest of the binding, PyTorch supplies device memory and streams, and everything is
 computed by the library's HIP kernels; this module checks tensors, fills the C structs and
@@ -521,8 +522,8 @@ def matmul_q8(x, weights, bias=None, alpha=None, residual=None, *, act="none", r
     each output).
 
     x [rows, in_features]: float32, bfloat16 or float16, rows at any stride, quantized by the call
-    as quantize_rows does (in the workspace, but for up to 4 rows of up to 8192 inputs), or Q8Rows. residual [rows,
-    out_features] in x's dtype, rows at any stride; bias, alpha (act="prelu"): float32
+    as quantize_rows does (in the workspace, but for up to 4 rows of up to 8192 inputs), or Q8Rows.
+    residual [rows, out_features] in x's dtype, rows at any stride; bias, alpha (act="prelu"): float32
     [out_features]. The epilogue is conv2d_fused's. The sums are exact. Returns y [rows,
     out_features] in x's dtype."""
     packed = isinstance(x, Q8Rows)

@@ -242,8 +242,8 @@ int q8_unpack(const void *packed, void *codes, float *scales, int rows, int in_f
  * rows, the epilogue that of conv2d_fused: bias, activation, and a residual before or after it.
  * The sums are exact; what follows is fp32, rounded once to y. The rows are x, quantized by the
  * call as quantize_rows does (it needs matmul_q8_workspace_size() bytes of workspace, 0 for a few
- * rows, or returns CONV2D_EUNSUPPORTED), or x_packed, for several products of the same rows. A row or an output
- * whose scale is NaN gives NaN. */
+ * rows, or returns CONV2D_EUNSUPPORTED), or x_packed, for several products of the same rows. A
+ * row or an output whose scale is NaN gives NaN. */
 typedef struct matmul_q8_args {
     const void *x;         /* [rows, in_features], rows x_row elements apart, or NULL */
     const void *x_packed;  /* where x is NULL: packed rows, with the same sizes */

@@ -29,6 +29,9 @@ CASES = [  # type, lengths, packed, channels, what else
     ("f32", [900, 900], False, 70, {"slots": [-1, 0]}),
     ("f32", [600, 1, 129], True, 33, {"coupled": False, "state": False}),
     ("bf16", [2049], False, 130, {"longest": 2049}),
+    # several rounds of workgroups, of equal sequences in chunks
+    ("f32", [900, 900, 900], False, 2056, {}),
+    ("bf16", [1100, 1100], False, 3330, {"coupled": False}),
     # many whole sequences, taken by length
     ("bf16", [(i * 37) % 101 for i in range(20)], True, 4101, {"slots": list(range(19, -1, -1)), "longest": 100}),
     ("f32", [3, 90, 0, 0, 90, 17, 90, 1, 64, 65, 2, 120, 119, 5, 77, 0, 31, 90], True, 2020, {"longest": 120}),

@@ -162,7 +162,9 @@ def test_workspace_sizes():
 def test_nothing_to_do_is_fine_without_a_device():
     assert _rec(nseq=0, x=0, forget=0, y=0) == c2d.OK
     assert _rec(step=True, nseq=0, x=0, forget=0, y=0) == c2d.OK
-    assert _back(size=False, nseq=0, grad_forget_bias=0) == c2d.OK
+    for tokens in (0, 1, 100, 1 << 20):
+        assert _rec(nseq=0, tokens=tokens) == c2d.OK and _rec(size=True, nseq=0, tokens=tokens) == 0
+        assert _back(size=False, nseq=0, tokens=tokens, grad_forget_bias=0) == c2d.OK and _back(nseq=0, tokens=tokens) == 0
 
 
 @pytest.mark.skipif(torch.cuda.device_count() > 0, reason="needs a machine without a GPU")
