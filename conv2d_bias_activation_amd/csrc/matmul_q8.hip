@@ -137,7 +137,8 @@ template <typename T> __device__ __forceinline__ u32x4 codes16(const Pack<T, 16>
 // WPR waves a row, so that few rows still make many waves, and ROWS neighbouring rows a workgroup,
 // whose 16-byte records make whole runs of 64 or 128 bytes. NR groups of 16 values of a lane stay
 // in registers between the maximum and the codes; a longer row is read again. The values behind
-// the last whole group go to a lane each.
+// the last whole group go to a lane each. 4096 x 4096 bf16 in 13.4 to 16 us (50 MB, 3.1 to 3.7 TB/s: HBM and the
+// vector ALU, some 14 instructions a value); 37 x 4010 in 4 us, a launch and two latencies.
 template <typename T, int WPR, int ROWS, int NR>
 __global__ __launch_bounds__(64 * WPR * ROWS) void quantize_kernel(const T *x, long long x_row, void *packed, int rows, int n) {
     __shared__ uint32_t s_most[WPR * ROWS];
@@ -265,7 +266,9 @@ __device__ __forceinline__ float behind_bias(float v, float alpha, float r, bool
 }
 
 // A few rows: a workgroup computes 16 NT outputs of 16 MT rows, straight from memory; its W waves
-// take the value blocks in turn and add up in LDS.
+// take the value blocks in turn and add up in LDS. The weights are read once for 16 MT rows and bound it
+// where they come from HBM: 37 x 4010 -> 10007 in 11.9 us, 3.4 TB/s; 8 x 2048 -> 4096 in 3.6 us, which is a launch and
+// two latencies.
 template <typename T, int NT, int MT, int W>
 __global__ __launch_bounds__(64 * W) void q8_few_kernel(const Q8Args a, int nblocks) {
     __shared__ i32x4 s_sum[W][NT * MT][64];
@@ -339,7 +342,8 @@ constexpr int kDirectWaves = 8, kDirectInputs = kDirectWaves * 64 * 16;  // a gr
 
 // Up to R rows that are not quantized yet, of at most kDirectInputs values: each workgroup does
 // that for itself, from L2, which costs less than a launch before this one, and keeps the codes
-// in LDS. The rest is as in q8_few_kernel; the first weights are on their way meanwhile.
+// in LDS. The rest is as in q8_few_kernel; the first weights are on their way meanwhile. 1 x 2048 -> 4096
+// in 3.9 us; with a launch of its own for the rows the call took 11.0 us, not 7.3.
 template <typename T, int R, int NT>
 __global__ __launch_bounds__(64 * kDirectWaves) void q8_direct_kernel(const Q8Args a, const T *xs, long long x_row, int inputs) {
     constexpr int W = kDirectWaves, U = 4, OUTS = NT * 16 * R;
@@ -447,6 +451,11 @@ __device__ __forceinline__ void q8_wave_lds() {
 
 // Many rows: BM rows x BN outputs a workgroup, WM x WN waves of 32x32 blocks, steps of one value
 // block through a ring of NS stages in LDS, loaded directly from memory.
+// 4096 x 4096 -> 16384 in 248 to 284 us (2100 TOP/s at 262), 8192 x 8192 -> 8192 in 457 (2400): under such a load the clock
+// falls to 1.7 GHz, and the matrix units are 59 to 66 % busy at it. What they miss is the start of a
+// workgroup and the end of its tile, some 11 us of 130 at 4096 inputs (one workgroup a CU: its
+// registers hold 256 x 256 sums). 333 x 2048 -> 4096 in 10.2 us on 64 x 64 tiles: 5 us are the launch and the first and
+// last steps, the rest the 256 KB that each workgroup brings into LDS.
 template <typename T, int BM, int BN, int WM, int WN, int NS, int KS>
 __global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(const Q8Args a, int tiles_m, int tiles_n) {
     constexpr int NW = WM * WN, FM = BM / (32 * WM), FN = BN / (32 * WN);
@@ -502,45 +511,45 @@ __global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(const Q8Args a, i
     const int at = (lane % 32 / 16) * kTileBytes + lane / 32 * 256 + lane % 16 * 16;
     if constexpr (KS == 1) {
 #pragma unroll
-    for (int s = 0; s < NS - 1; s++) issue(s, 0, LPW);
+        for (int s = 0; s < NS - 1; s++) issue(s, 0, LPW);
         i32x4 xf[2][FM], wf[2][FN];
-    // Operand f of half h of step kb from LDS: the weights', then the rows'.
-    auto read = [&](int kb, int h, int f0, int f1) {
-        const char *st = lds + kb % NS * STAGE + h * 512 + at;
+        // Operand f of half h of step kb from LDS: the weights', then the rows'.
+        auto read = [&](int kb, int h, int f0, int f1) {
+            const char *st = lds + kb % NS * STAGE + h * 512 + at;
 #pragma unroll
-        for (int f = f0; f < f1; f++) {
-            if (f < FN)
-                wf[h][f] = *reinterpret_cast<const i32x4 *>(st + BM * kVals + (wn * FN + f) * 2 * kTileBytes);
-            else if (f < FN + FM)
-                xf[h][f - FN] = *reinterpret_cast<const i32x4 *>(st + (wm * FM + f - FN) * 2 * kTileBytes);
-        }
-    };
-    // The products of half h of step kb, with the operands of the next half read, and the step
-    // NS - 1 ahead loaded, between them: the order is kept as written, as the compiler would read
-    // the operands last and wait for them.
-    constexpr int RG = (FM + FN + FM - 1) / FM, DG = (LPW + FM - 1) / FM;
-    auto half = [&](int kb, auto hc) {
-        constexpr int h = decltype(hc)::value;
+            for (int f = f0; f < f1; f++) {
+                if (f < FN)
+                    wf[h][f] = *reinterpret_cast<const i32x4 *>(st + BM * kVals + (wn * FN + f) * 2 * kTileBytes);
+                else if (f < FN + FM)
+                    xf[h][f - FN] = *reinterpret_cast<const i32x4 *>(st + (wm * FM + f - FN) * 2 * kTileBytes);
+            }
+        };
+        // The products of half h of step kb, with the operands of the next half read, and the step
+        // NS - 1 ahead loaded, between them: the order is kept as written, as the compiler would read
+        // the operands last and wait for them.
+        constexpr int RG = (FM + FN + FM - 1) / FM, DG = (LPW + FM - 1) / FM;
+        auto half = [&](int kb, auto hc) {
+            constexpr int h = decltype(hc)::value;
 #pragma unroll
-        for (int m = 0; m < FM; m++) {
-            if constexpr (h == 1) issue(kb + NS - 1, m * DG, min((m + 1) * DG, LPW));
-            // all reads in the first half of the products
-            read(kb + h, 1 - h, m * 2 * RG, (m + 1) * 2 * RG);
+            for (int m = 0; m < FM; m++) {
+                if constexpr (h == 1) issue(kb + NS - 1, m * DG, min((m + 1) * DG, LPW));
+                // all reads in the first half of the products
+                read(kb + h, 1 - h, m * 2 * RG, (m + 1) * 2 * RG);
 #pragma unroll
-            for (int n = 0; n < FN; n++) acc[m][n] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[h][n], xf[h][m], acc[m][n], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    };
-    // The barrier that hands out the next stage stands between a step's halves.
-    q8_wait_vmcnt<(NS - 2) * LPW>();
-    q8_barrier();
-    read(0, 0, 0, FM + FN);
-    for (int kb = 0; kb < KB; kb++) {
-        half(kb, std::integral_constant<int, 0>{});
-        q8_wait_vmcnt<(NS - 3) * LPW>();
+                for (int n = 0; n < FN; n++) acc[m][n] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[h][n], xf[h][m], acc[m][n], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        // The barrier that hands out the next stage stands between a step's halves.
+        q8_wait_vmcnt<(NS - 2) * LPW>();
         q8_barrier();
-        half(kb, std::integral_constant<int, 1>{});
-    }
+        read(0, 0, 0, FM + FN);
+        for (int kb = 0; kb < KB; kb++) {
+            half(kb, std::integral_constant<int, 0>{});
+            q8_wait_vmcnt<(NS - 3) * LPW>();
+            q8_barrier();
+            half(kb, std::integral_constant<int, 1>{});
+        }
     } else {
         // Small tiles: the operands of a whole step are read while those of the step before are
         // multiplied, so that a step waits for one barrier and for no read. A stage is free for
