@@ -732,7 +732,10 @@ struct Costs {
 //   8 x 4096 x 2048                  170 / 133         513 / 305
 //   8 x 4096 x 2176                  178 / 157         460 / 343
 //   16 x 2048 x 2176                 159 / 152         410 / 350
-//   16 x 2048 x 4096, ragged         274 / 310         590 / 659
+//   16 x 2048 x 4096, ragged         238 / 341         573 / 694
+//   64 x 250 x 1500, ragged           65 /  73         165 / 202
+//   40 x 1000 x 2112, ragged         194 / 211         474 / 554
+//   32 x 1000 x 1000, ragged         121 /  93         324 / 243
 //   1 x 65536 x 1024                2520 / 148        7030 / 307
 constexpr Costs kPrompt{3.0, 9.0, 2.2, 4.0, 4.7, true}, kGradient{8.0, 17.0, 5.8, 9.0, 10.3, false};
 
@@ -787,7 +790,8 @@ template <typename Args> RecCut cut(const Args &a, int vec, const Costs &costs, 
     const double walk = 1.3 * costs.tile_us * (double)tiles * (ragged ? 1.0 : rounds(wide));
     const double whole = costs.fixed_whole + std::max(walk, costs.moved_whole * value_us);
     if (may_split && wide && whole > costs.fixed_split + costs.moved_split * value_us) {
-        double factor = 1.0;
+        // ragged: a sequence's last chunk is as short as it comes
+        double factor = 1.1 + 0.5 * (double)wide / kRaggedWorkgroups;
         const long long run = ragged ? std::max((total * k.cblocks + kRaggedWorkgroups * kTile - 1) / (kRaggedWorkgroups * kTile), 1ll)
                                      : best_run(tiles, wide, &factor);
         if (run < tiles && whole > costs.fixed_split + costs.moved_split * value_us * factor) k.run = (int)(run * kTile);
