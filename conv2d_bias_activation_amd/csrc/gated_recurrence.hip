@@ -42,6 +42,7 @@ struct RecCut {
     int chunks;   // unpacked: chunks of a sequence
     int cblocks;  // blocks of 64 VEC channels
     int ranked;   // whole packed sequences: how many stand side by side on the card, else 0
+    int near;     // blocks of channels of the same tokens stand on one XCD
     float *rec;   // split sequences: records of the chunks, [item][fields][channels]
     float *tile;  // gradient: [tile number][2][channels]
     float *bias;  // gradient: sums of grad_forget, [item][channels]
@@ -55,6 +56,18 @@ struct RecCut {
 //       cannot read from the state row any more, where another workgroup leaves the new one
 //   kD: gradient: carry at the chunk's first token, from zero; last chunk: from the final one
 enum { kA, kB, kD };
+
+// The workgroup's chunk number and its block of channels. Workgroups go to the XCDs in turn; with `near` eight
+// numbers at a time are given out, one to each XCD, with all their blocks, which share cache lines.
+struct Slot {
+    int item, cblock;
+};
+__device__ __forceinline__ Slot slot_of(const RecCut &k) {
+    const int b = blockIdx.x, even = k.near ? k.items / 8 * 8 : 0;
+    if (b >= even * k.cblocks) return {b / k.cblocks, b % k.cblocks};
+    const int j = b / 8;
+    return {j / k.cblocks * 8 + b % 8, j % k.cblocks};
+}
 
 // Where a workgroup stands.
 struct Place {
@@ -205,8 +218,8 @@ template <typename T, int VEC, bool COUPLED>
 __global__ __launch_bounds__(64 * kNW) void rec_first_kernel(const gated_recurrence_args a, const RecCut k) {
     __shared__ float2 s_run[kNW][VEC][64];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int item = blockIdx.x / k.cblocks;
-    const auto [c, own] = channels_of<VEC>(((int)(blockIdx.x % k.cblocks) * 64 + lane) * VEC, a.channels);
+    const auto [item, cblock] = slot_of(k);
+    const auto [c, own] = channels_of<VEC>((cblock * 64 + lane) * VEC, a.channels);
     Place p;
     if (!place_of(a, k, item, p) || p.chunk == p.last) return;  // so the chunk is a whole run
     const T *x = rows<T>(a.x, p, a.x_batch, a.x_token), *forget = rows<T>(a.forget, p, a.forget_batch, a.forget_token);
@@ -283,10 +296,10 @@ __global__ __launch_bounds__(64 * kNW, 4) void rec_prompt_kernel(const gated_rec
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     // the second pass takes the chunks that the first read last first: they may still be cached
     __shared__ int s_found;
-    const int place = blockIdx.x / k.cblocks;
+    const auto [place, cblock] = slot_of(k);
     const int item = k.ranked ? by_length(a.offsets, a.nseq, (int)a.tokens, place, k.ranked, reinterpret_cast<uint64_t *>(s_run), s_found)
                               : k.items - 1 - place;
-    const auto [c, own] = channels_of<VEC>(((int)(blockIdx.x % k.cblocks) * 64 + lane) * VEC, a.channels);
+    const auto [c, own] = channels_of<VEC>((cblock * 64 + lane) * VEC, a.channels);
     Place p;
     if (!place_of(a, k, item, p)) return;
 
@@ -389,9 +402,9 @@ __global__ __launch_bounds__(64 * kNW) void rec_back_first_kernel(const gated_re
     __shared__ float4 s_run[2][kNW][VEC][64];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     __shared__ int s_found;
-    int item = blockIdx.x / k.cblocks;
+    auto [item, cblock] = slot_of(k);
     if (k.ranked) item = by_length(a.offsets, a.nseq, (int)a.tokens, item, k.ranked, reinterpret_cast<uint64_t *>(s_run), s_found);
-    const auto [c, own] = channels_of<VEC>(((int)(blockIdx.x % k.cblocks) * 64 + lane) * VEC, a.channels);
+    const auto [c, own] = channels_of<VEC>((cblock * 64 + lane) * VEC, a.channels);
     Place p;
     if (!place_of(a, k, item, p)) return;
     const bool split = p.last > 0;
@@ -504,10 +517,10 @@ __global__ __launch_bounds__(64 * kNW) void rec_back_kernel(const gated_recurren
     __shared__ float4 s_run[2][kNW][VEC][64];
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     __shared__ int s_found;
-    const int place = blockIdx.x / k.cblocks;
+    const auto [place, cblock] = slot_of(k);
     const int item = k.ranked ? by_length(a.offsets, a.nseq, (int)a.tokens, place, k.ranked, reinterpret_cast<uint64_t *>(s_run), s_found)
                               : k.items - 1 - place;
-    const auto [c, own] = channels_of<VEC>(((int)(blockIdx.x % k.cblocks) * 64 + lane) * VEC, a.channels);
+    const auto [c, own] = channels_of<VEC>((cblock * 64 + lane) * VEC, a.channels);
     float sum[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; v++) sum[v] = 0.0f;
@@ -798,6 +811,14 @@ template <typename Args> RecCut cut(const Args &a, int vec, const Costs &costs, 
     }
     k.chunks = a.offsets ? 0 : (int)std::max((a.tokens + k.run - 1) / k.run, 1ll);
     k.items = a.offsets ? (int)(a.tokens / k.run + a.nseq) : k.chunks * a.nseq;
+    // Rows that do not start on cache lines share them between blocks of channels. On one XCD and on any, us,
+    // prompt / gradient: 5 x 3000 x 1500 60 / 132 and 68 / 144, 8 x 4096 x 2050 161 / 406 and 183 / 432, 32 ragged
+    // sequences of 32000 x 1000 84 / 236 and 93 / 243. Rows on lines: 8 x 4096 x 2048 130 / 309 and 131 / 306; few ragged
+    // chunks fill the XCDs unevenly (6 sequences of 20000 x 2560 133 / 309 and 116 / 266), and small calls have little
+    // to share (1 x 999 x 250 13 / 18 and 10 / 16). The other rows are taken to stand as x and forget do.
+    const uintptr_t lines = (uintptr_t)a.x | (uintptr_t)a.forget | (uintptr_t)(a.x_token * dtype_bytes(a.dtype)) |
+                            (uintptr_t)(a.forget_token * dtype_bytes(a.dtype));
+    k.near = lines % 128 != 0 && value_us > 1.0 && (!ragged || k.items >= 64);
     // the order costs each workgroup a look at all lengths, which long sequences earn back
     if (a.offsets && k.run == kWhole && k.items == a.nseq && a.nseq <= kMaxRanked && wide > kWorkgroups &&
         a.tokens >= 2ll * a.nseq * a.nseq)
