@@ -509,9 +509,10 @@ __global__ __launch_bounds__(64 * kNW) void rec_back_first_kernel(const gated_re
 
 // The second pass walks backwards over the tiles and writes the gradients: the states before each
 // token again from the tile's, and the carry against them, both composed over the waves from the
-// same LDS records. WHOLE: the channels fill their blocks. Four inputs on their way and four values
-// a token kept take 256 registers, so one workgroup a CU. HBM: 8 x 4096 x 2048 bf16 in 184 us, 5.1 TB/s, the
-// vector ALU 53 % busy.
+// same LDS records. Four inputs on their way and four values a token kept take 256 registers, so one
+// workgroup a CU. HBM: 8 x 4096 x 2048 bf16 in 184 us, 5.1 TB/s, the vector ALU 53 % busy. WHOLE: the channels
+// fill their blocks, which all waves would ask otherwise (a gradient of 8 x 4096 x 2048 in 313 us, not 323); else the
+// waves whose lanes all own theirs still store without a look at each (8 x 4096 x 2112 352 us, not 392).
 template <typename T, int VEC, bool WHOLE, bool GATED>
 __global__ __launch_bounds__(64 * kNW) void rec_back_kernel(const gated_recurrence_backward_args a, const RecCut k) {
     __shared__ float4 s_run[2][kNW][VEC][64];
@@ -521,6 +522,7 @@ __global__ __launch_bounds__(64 * kNW) void rec_back_kernel(const gated_recurren
     const int item = k.ranked ? by_length(a.offsets, a.nseq, (int)a.tokens, place, k.ranked, reinterpret_cast<uint64_t *>(s_run), s_found)
                               : k.items - 1 - place;
     const auto [c, own] = channels_of<VEC>((cblock * 64 + lane) * VEC, a.channels);
+    const bool whole = WHOLE || all_own<VEC>(own);
     float sum[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; v++) sum[v] = 0.0f;
@@ -648,10 +650,17 @@ __global__ __launch_bounds__(64 * kNW) void rec_back_kernel(const gated_recurren
                 if (t + i < p.end) sum[v] += d;
             }
             if (t + i < p.end) {
-                const int part = WHOLE ? VEC : own;
-                put<T, VEC>(gx + (t + i) * a.grad_x_token + (unsigned)c, ox, part);
-                put<T, VEC>(gf + (t + i) * a.grad_forget_token + (unsigned)c, of, part);
-                if constexpr (GATED) put<T, VEC>(gg + (t + i) * a.grad_gate_token + (unsigned)c, og, part);
+                T *px = gx + (t + i) * a.grad_x_token + (unsigned)c, *pf = gf + (t + i) * a.grad_forget_token + (unsigned)c, *pg;
+                if constexpr (GATED) pg = gg + (t + i) * a.grad_gate_token + (unsigned)c;
+                if (whole) {
+                    put<T, VEC>(px, ox);
+                    put<T, VEC>(pf, of);
+                    if constexpr (GATED) put<T, VEC>(pg, og);
+                } else {
+                    put<T, VEC>(px, ox, own);
+                    put<T, VEC>(pf, of, own);
+                    if constexpr (GATED) put<T, VEC>(pg, og, own);
+                }
             }
         }
         buf ^= 1;
@@ -859,13 +868,18 @@ template <typename T, int VEC> hipError_t launch_back(const gated_recurrence_bac
     const long long blocks = (long long)k.items * k.cblocks, bias_blocks = (a.channels + 63) / 64;
     if (a.grad_forget_bias && bias_blocks > 0xffffffffll / 1024) return hipErrorInvalidConfiguration;  // before any launch
     hipError_t e = hipSuccess;
-    if (blocks)
-        e = by_form(a.channels % (64 * VEC) == 0, a.gate, [&](auto whole, auto gated) {
-            constexpr bool W = decltype(whole)::value, G = decltype(gated)::value;
-            const hipError_t e1 = k.rec ? launch_blocks(rec_back_first_kernel<T, VEC, G, true>, blocks, 64 * kNW, st, a, k)
-                                        : launch_blocks(rec_back_first_kernel<T, VEC, false, false>, blocks, 64 * kNW, st, a, k);
-            return e1 != hipSuccess ? e1 : launch_blocks(rec_back_kernel<T, VEC, W, G>, blocks, 64 * kNW, st, a, k);
-        });
+    if (blocks) {
+        if (!k.rec)
+            e = launch_blocks(rec_back_first_kernel<T, VEC, false, false>, blocks, 64 * kNW, st, a, k);
+        else if (a.gate)
+            e = launch_blocks(rec_back_first_kernel<T, VEC, true, true>, blocks, 64 * kNW, st, a, k);
+        else
+            e = launch_blocks(rec_back_first_kernel<T, VEC, false, true>, blocks, 64 * kNW, st, a, k);
+        if (e == hipSuccess)
+            e = by_form(a.channels % (64 * VEC) == 0, a.gate, [&](auto whole, auto gated) {
+                return launch_blocks(rec_back_kernel<T, VEC, decltype(whole)::value, decltype(gated)::value>, blocks, 64 * kNW, st, a, k);
+            });
+    }
     if (e == hipSuccess && a.grad_forget_bias)
         e = launch_blocks(rec_bias_kernel, bias_blocks, 1024, st, k.bias, a.grad_forget_bias, k.items, a.channels);
     return e;
