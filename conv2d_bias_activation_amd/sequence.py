@@ -352,8 +352,8 @@ def gated_recurrence_backward(grad, x, forget, *, gate=None, forget_bias=None, c
     float32 [rows, channels] is updated in place, from the gradient of the state that a sequence
     left to that of the state it started from (None: the states left are of no further use).
     ``out``: tensors (grad_x, grad_forget, grad_gate or None) to write, which may be column slices
-    of one tensor; grad_forget_bias is float32 and always new. Needs a workspace, so no
-    ``workspace=False``."""
+    of one tensor; grad_forget_bias is float32 and always new. ``workspace`` as for selective_scan,
+    but the call needs one, so not False."""
     dt = _storage(x)
     dev, dtype, shape = x.device, x.dtype, x.shape
     nseq, tokens, *x_strides = _geometry(x, seq_offsets, False)
@@ -524,8 +524,9 @@ def matmul_q8(x, weights, bias=None, alpha=None, residual=None, *, act="none", r
     x [rows, in_features]: float32, bfloat16 or float16, rows at any stride, quantized by the call
     as quantize_rows does (in the workspace, but for up to 4 rows of up to 8192 inputs), or Q8Rows.
     residual [rows, out_features] in x's dtype, rows at any stride; bias, alpha (act="prelu"): float32
-    [out_features]. The epilogue is conv2d_fused's. The sums are exact. Returns y [rows,
-    out_features] in x's dtype."""
+    [out_features]. The epilogue is conv2d_fused's. The sums are exact. ``workspace`` as for
+    selective_scan; False only where the call needs none. Returns y [rows, out_features] in x's
+    dtype."""
     packed = isinstance(x, Q8Rows)
     dev, dtype, n, k = weights.device, x.dtype, weights.rows, weights.in_features
     if packed:

@@ -32,6 +32,9 @@ CASES = [  # type, lengths, packed, channels, what else
     # several rounds of workgroups, of equal sequences in chunks
     ("f32", [900, 900, 900], False, 2056, {}),
     ("bf16", [1100, 1100], False, 3330, {"coupled": False}),
+    # many sequences whose rows share cache lines between blocks of channels; the second lot taken by length, too
+    ("bf16", [(i * 29) % 83 for i in range(70)], True, 1001, {"longest": 82}),
+    ("f16", [(i * 53) % 257 + 9 * (i % 3) for i in range(64)], True, 701, {"longest": 274, "slots": list(range(63, -1, -1))}),
     # many whole sequences, taken by length
     ("bf16", [(i * 37) % 101 for i in range(20)], True, 4101, {"slots": list(range(19, -1, -1)), "longest": 100}),
     ("f32", [3, 90, 0, 0, 90, 17, 90, 1, 64, 65, 2, 120, 119, 5, 77, 0, 31, 90], True, 2020, {"longest": 120}),
