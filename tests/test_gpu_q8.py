@@ -155,6 +155,13 @@ PRODUCTS = [  # type, rows, inputs, outputs, what else
     ("f16", 1, 8191, 16391, {"residual": True, "before": True}),
     ("bf16", 4, 8193, 40, {}),
     ("f16", 2, 17, 5, {"act": "silu"}),
+    # every size of tile, with rows, inputs and outputs that end inside one
+    ("bf16", 333, 1000, 4090, {"bias": True, "residual": True}),
+    ("f32", 340, 65, 4096, {}),
+    ("f32", 4090, 70, 2039, {"act": "silu", "bias": True}),
+    ("f16", 4090, 129, 2040, {"wide": 8, "bias": True}),
+    ("bf16", 2040, 130, 8190, {"residual": True, "act": "relu"}),
+    ("f32", 2047, 64, 8191, {"bias": True, "residual": True, "before": True, "act": "prelu"}),
 ]
 
 
