@@ -454,7 +454,7 @@ __device__ __forceinline__ void q8_wave_lds() {
 // 4096 x 4096 -> 16384 in 248 to 284 us (2100 TOP/s at 262), 8192 x 8192 -> 8192 in 457 (2400): under such a load the clock
 // falls to 1.7 GHz, and the matrix units are 59 to 66 % busy at it. What they miss is the start of a
 // workgroup and the end of its tile, some 11 us of 130 at 4096 inputs (one workgroup a CU: its
-// registers hold 256 x 256 sums). 333 x 2048 -> 4096 in 10.2 us on 64 x 64 tiles: 5 us are the launch and the first and
+// registers hold 256 x 256 sums). 333 x 2048 -> 4096 in 9.9 us on 64 x 64 tiles: 5 us are the launch and the first and
 // last steps, the rest the 256 KB that each workgroup brings into LDS.
 template <typename T, int BM, int BN, int WM, int WN, int NS, int KS>
 __global__ __launch_bounds__(64 * WM * WN) void q8_tile_kernel(const Q8Args a, int tiles_m, int tiles_n) {

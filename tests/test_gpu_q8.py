@@ -270,6 +270,26 @@ def test_offsets_past_32_bits():
     assert torch.equal(out, want)
 
 
+def test_packed_rows_past_2_gib():
+    """Weights whose packed bytes pass 2^31: their last rows, and the outputs that read them."""
+    n, k, tail = 140001, 16384, 40
+    g = torch.Generator(device=DEV).manual_seed(11)
+    w = torch.randn(n, k, generator=g, device=DEV, dtype=torch.bfloat16)
+    weights = c2d.quantize_rows(w)
+    assert weights.data.numel() > 1 << 31
+    wcodes, wscales = quantized(w[-tail:].cpu())
+    codes, scales = c2d.q8_unpack(weights)
+    assert torch.equal(codes[-tail:].cpu(), wcodes) and torch.equal(scales[-tail:].cpu(), wscales)
+    again = c2d.q8_pack(codes, scales)
+    assert torch.equal(again.data, weights.data)
+    del again, codes, w
+    for rows in (1, 30, 600):
+        x = _normal(rows, rows, k, dtype=torch.bfloat16)
+        want, bound = product(*quantized(x), wcodes, wscales, torch.bfloat16)
+        y = c2d.matmul_q8(_on(x), weights)
+        ref.close(y[:, -tail:], want, bound, f"{rows} rows")
+
+
 def test_product_needs_a_workspace_or_packed_rows():
     x = _on(_normal(1, 20, 64))
     w = c2d.q8_pack(*map(_on, _weights(1, 8, 64)))
