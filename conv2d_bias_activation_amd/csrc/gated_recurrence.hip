@@ -21,13 +21,13 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// keep = sigmoid(z) and take = 1 - sigmoid(z) for z = v + bias, scaled = -log2(e) bias; both to
-// full relative precision. Where exp(-z) is infinite its product with 0 is not a number, of which
-// the minimum with 1 is 1, as it should be; a z that is not a number makes keep one too.
+// keep = sigmoid(z) and take = 1 - sigmoid(z) for z = v + bias, scaled = -log2(e) bias. The reciprocal gives no numbers
+// below the smallest normal one: keep is 0 for z under some -87.3, and take, whose product would be 0 or not a number, is
+// 1 there. A z that is not a number makes both one.
 __device__ __forceinline__ void gates(float v, float scaled, float &keep, float &take) {
     const float t = __builtin_amdgcn_exp2f(fmaf(v, -kLog2e, scaled));
     keep = __builtin_amdgcn_rcpf(1.0f + t);
-    take = fminf(t * keep, 1.0f);
+    take = keep == 0.0f ? 1.0f : t * keep;
 }
 
 constexpr int kTW = 8;          // neighbouring tokens of a wave
