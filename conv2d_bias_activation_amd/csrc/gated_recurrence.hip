@@ -21,11 +21,13 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// keep = sigmoid(z) and take = 1 - sigmoid(z) for z = v + bias, scaled = -log2(e) bias. The reciprocal gives no numbers
-// below the smallest normal one: keep is 0 for z under some -87.3, and take, whose product would be 0 or not a number, is
-// 1 there. A z that is not a number makes both one.
-__device__ __forceinline__ void gates(float v, float scaled, float &keep, float &take) {
-    const float t = __builtin_amdgcn_exp2f(fmaf(v, -kLog2e, scaled));
+// keep = sigmoid(z) and take = 1 - sigmoid(z) for z = forget + bias, which is added before anything else, as the two may
+// cancel. With u = 2^-24, exp2's argument is off by up to 1.5 u |z| and its value by two roundings, so keep is off by
+// u ((2.5 |z| + 2) take + 3) of itself, the sum's rounding counted, and take by u ((2.5 |z| + 2) keep + 4). The
+// reciprocal gives no numbers below the smallest normal one: keep is 0 for z under some -87.3, and take, whose product would be 0
+// or not a number, is 1 there. A z that is not a number makes both one.
+__device__ __forceinline__ void gates(float z, float &keep, float &take) {
+    const float t = __builtin_amdgcn_exp2f(-kLog2e * z);
     keep = __builtin_amdgcn_rcpf(1.0f + t);
     take = keep == 0.0f ? 1.0f : t * keep;
 }
@@ -232,7 +234,7 @@ __global__ __launch_bounds__(64 * kNW) void rec_first_kernel(const gated_recurre
     }
     float bias[VEC] = {};
 #pragma unroll
-    for (int v = 0; v < VEC; v++) bias[v] = a.forget_bias ? -kLog2e * a.forget_bias[c + v] : 0.0f;
+    for (int v = 0; v < VEC; v++) bias[v] = a.forget_bias ? a.forget_bias[c + v] : 0.0f;
     float At[VEC], Bt[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; v++) At[v] = 1.0f, Bt[v] = 0.0f;
@@ -249,7 +251,7 @@ __global__ __launch_bounds__(64 * kNW) void rec_first_kernel(const gated_recurre
 #pragma unroll
             for (int v = 0; v < VEC; v++) {
                 float take;
-                gates(to_f32(nf[i].v[v]), bias[v], f[i][v], take);
+                gates(to_f32(nf[i].v[v]) + bias[v], f[i][v], take);
                 b[i][v] = COUPLED ? to_f32(nx[i].v[v]) * take : to_f32(nx[i].v[v]);
             }
         if (t + kTW < t1) {
@@ -312,8 +314,6 @@ __global__ __launch_bounds__(64 * kNW, 4) void rec_prompt_kernel(const gated_rec
 
     Floats<VEC> bias{}, h{};
     if (a.forget_bias) bias = get<float, VEC>(a.forget_bias + c);
-#pragma unroll
-    for (int v = 0; v < VEC; v++) bias.v[v] *= -kLog2e;
     if (p.last == 0 && state && !a.fresh) h = get<float, VEC>(state);
 
     Pack<T, VEC> nx[kTW], nf[kTW], ng[kTW];
@@ -345,7 +345,7 @@ __global__ __launch_bounds__(64 * kNW, 4) void rec_prompt_kernel(const gated_rec
 #pragma unroll
             for (int v = 0; v < VEC; v++) {
                 float take;
-                gates(to_f32(nf[i].v[v]), bias.v[v], f[i][v], take);
+                gates(to_f32(nf[i].v[v]) + bias.v[v], f[i][v], take);
                 b[i][v] = COUPLED ? to_f32(nx[i].v[v]) * take : to_f32(nx[i].v[v]);
                 if (!kFull && t + i >= p.end) f[i][v] = 1.0f, b[i][v] = 0.0f;
                 B[v] = fmaf(f[i][v], B[v], b[i][v]);
@@ -417,8 +417,6 @@ __global__ __launch_bounds__(64 * kNW) void rec_back_first_kernel(const gated_re
 
     Floats<VEC> bias{}, h{}, carry{};
     if (a.forget_bias) bias = get<float, VEC>(a.forget_bias + c);
-#pragma unroll
-    for (int v = 0; v < VEC; v++) bias.v[v] *= -kLog2e;
     if (p.chunk == 0) {
         const int row = state_row(a.state, a.slots, p.r.seq, a.state_rows);
         if (row >= 0) h = get<float, VEC>(a.state + (long long)row * a.channels + c);
@@ -461,7 +459,7 @@ __global__ __launch_bounds__(64 * kNW) void rec_back_first_kernel(const gated_re
 #pragma unroll
             for (int v = 0; v < VEC; v++) {
                 float f, take;
-                gates(to_f32(nf[i].v[v]), bias.v[v], f, take);
+                gates(to_f32(nf[i].v[v]) + bias.v[v], f, take);
                 float b = to_f32(nx[i].v[v]) * (a.coupled ? take : 1.0f);
                 if (t + i >= p.end) f = 1.0f, b = 0.0f;
                 B[v] = fmaf(f, B[v], b);
@@ -544,8 +542,6 @@ __global__ __launch_bounds__(64 * kNW) void rec_back_kernel(const gated_recurren
 
     Floats<VEC> bias{}, before{}, carry{};  // state before the chunk, gradient carried into the tile
     if (a.forget_bias) bias = get<float, VEC>(a.forget_bias + c);
-#pragma unroll
-    for (int v = 0; v < VEC; v++) bias.v[v] *= -kLog2e;
 
     Pack<T, VEC> nx[kTW], nf[kTW], ng[kTW], ne[kTW];
     Floats<VEC> na, nb;
@@ -588,13 +584,13 @@ __global__ __launch_bounds__(64 * kNW) void rec_back_kernel(const gated_recurren
 #pragma unroll
             for (int v = 0; v < VEC; v++) {
                 xs[i][v] = to_f32(nx[i].v[v]);
-                gates(to_f32(nf[i].v[v]), bias.v[v], f[i][v], take[i][v]);
+                gates(to_f32(nf[i].v[v]) + bias.v[v], f[i][v], take[i][v]);
                 e[i][v] = to_f32(ne[i].v[v]);
                 dz[i][v] = 0.0f;
                 if constexpr (GATED) {
                     const float g = to_f32(ng[i].v[v]);
                     float up, down;
-                    gates(g, 0.0f, up, down);
+                    gates(g, up, down);
                     dz[i][v] = e[i][v] * up * fmaf(g, down, 1.0f);
                     e[i][v] *= g * up;
                 }
@@ -723,7 +719,7 @@ __global__ __launch_bounds__(kBlock) void rec_token_kernel(const gated_recurrenc
 #pragma unroll
     for (int v = 0; v < VEC; v++) {
         float keep, take;
-        gates(to_f32(z.v[v]), -kLog2e * bias.v[v], keep, take);
+        gates(to_f32(z.v[v]) + bias.v[v], keep, take);
         h.v[v] = fmaf(keep, h.v[v], to_f32(x.v[v]) * (a.coupled ? take : 1.0f));
         y.v[v] = round_fp32<T>(a.gate ? h.v[v] * activate_c<CONV2D_ACT_SILU>(to_f32(gate.v[v]), 0.0f) : h.v[v]);
     }

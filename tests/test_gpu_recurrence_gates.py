@@ -70,3 +70,19 @@ def test_gates_next_to_their_ends(monkeypatch, kind, coupled, bias):
     """Logits past 87, where a gate leaves the normal numbers: the other one is 1."""
     b = None if bias is None else torch.full((len(ENDS),), bias)
     _check(monkeypatch, kind, [70, 1, 600], ENDS if bias is None else ENDS - bias, b, coupled, 1)
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("coupled", [True, False])
+def test_logits_and_biases_that_cancel(monkeypatch, kind, coupled):
+    """The gate goes by the sum alone, however large its two terms are."""
+    g = torch.Generator().manual_seed(5)
+    size = torch.cat([torch.tensor([100.0]).expand(40), torch.tensor([1000.0]).expand(40), torch.tensor([1e4]).expand(20)])
+    v = torch.cat([(torch.rand(100, generator=g) * 2 - 1) * size,
+                   torch.tensor([100.0, -100.0, 5e4, 2.3e38, 2.5e38, -2.5e38, 3e38, -3e38])])
+    if kind == "f16":
+        v = v.clamp(-6e4, 6e4)
+    v = v.to(TYPES[kind]).float()
+    bias = torch.randn(len(v), generator=g) * 2 - v
+    bias[100:] = -v[100:]
+    _check(monkeypatch, kind, [70, 1, 600], v, bias, coupled, 2)
