@@ -267,7 +267,7 @@ __device__ __forceinline__ float behind_bias(float v, float alpha, float r, bool
 
 // A few rows: a workgroup computes 16 NT outputs of 16 MT rows, straight from memory; its W waves
 // take the value blocks in turn and add up in LDS. The weights are read once for 16 MT rows and bound it
-// where they come from HBM: 37 x 4010 -> 10007 in 11.9 us, 3.4 TB/s; 8 x 2048 -> 4096 in 3.6 us, which is a launch and
+// where they come from HBM: 64 x 4010 -> 8192 in 13.0 us, 2.5 TB/s; 8 x 2048 -> 4096 in 3.6 us, which is a launch and
 // two latencies.
 template <typename T, int NT, int MT, int W>
 __global__ __launch_bounds__(64 * W) void q8_few_kernel(const Q8Args a, int nblocks) {
@@ -707,18 +707,23 @@ template <typename T> hipError_t launch_direct(const Q8Args &p, const matmul_q8_
                                              : direct<T, 4, 1>(p, a.x, a.x_row, a.in_features, st);
 }
 
-// Which kernel and tile. Up to 2048 blocks of 16 x 16 the operands come straight from memory, from
-// there on through LDS. Times in us, weights not in L2, few-rows kernels by their NT, MT, W, tiles
-// by rows x outputs:
-//   rows x inputs -> outputs    1,1,8  2,1,8  2,2,8  64x64 64x128 128x128
-//       8 x  2048 ->  4096        3.6    4.2    4.7    6.5    9.0   10.0
-//       8 x  8192 -> 16384       27.1   23.5   24.3   25.1   44.8   47.4
-//      37 x  4010 -> 10007       20.0   19.3   15.0   12.4               (2,4,8: 11.9)
-//      32 x  2048 ->  4096        4.0    4.2    5.0    7.1   10.8   11.6
-//      32 x  8192 -> 16384       43.5   35.3   26.3   26.0   46.4   49.5
-//     128 x  2048 ->  4096        7.6    6.4    6.2    7.5   11.0   14.2
-//      64 x  4096 -> 11008       22.3   16.8   12.1   11.6   18.1   21.4
-//     256 x  2048 ->  4096       12.9   10.4    9.0    8.2   11.5   14.4
+// Which kernel and tile. A few-rows kernel, whose operands come straight from memory, for rows and outputs that make at most two
+// of its workgroups a CU; from there on tiles, through LDS. Times in us, weights not in the caches, few-rows kernels by their
+// NT, MT, W, tiles by rows x outputs; the last column has the workgroups of 2,2,8:
+//   rows x inputs -> outputs    1,1,8  2,1,8  2,2,8  64x64 128x128
+//       8 x  2048 ->  4096        3.6    4.2    4.7    6.5   10.0
+//       8 x  8192 -> 16384       27.1   23.5   24.3   25.1   47.4
+//      32 x  2048 ->  4096        4.0    4.2    5.0    7.1   11.6
+//      33 x  2048 ->  8192                      7.2    7.9            512
+//      64 x  4010 ->  8192                     13.0   14.4            512
+//      20 x  4010 -> 16384                     15.2   16.4            512
+//     128 x  2048 ->  4096        7.6    6.4    6.2    7.2   14.2     512
+//      90 x  4010 ->  6000                     13.6   12.7            564
+//      33 x  2048 -> 10007                     10.1    8.7            626
+//      37 x  4010 -> 10007                     16.5   14.2            626
+//      48 x  8192 -> 10007                     28.8   24.0            626
+//      33 x  4010 -> 13000                     20.0   15.1            814
+//     256 x  2048 ->  4096       12.9   10.4    9.0    8.2   14.4    1024
 // Among the tiles the one is taken whose workgroups, spread over the 256 CUs, take the least time
 // by what a step of 64 inputs of one takes where the card is full: 64x64 0.11 us, 64x128 0.22,
 // 128x128 0.30, 128x256 0.55, 256x256 0.87. Larger tiles read each operand less often; smaller ones
@@ -730,7 +735,7 @@ template <typename T> hipError_t launch_product(const Q8Args &a, hipStream_t st)
     const long long n = row_tiles(a.outs), m = row_tiles(a.rows);
     if (m == 1) return n >= 1024 ? few<T, 2, 1, 8>(a, st) : few<T, 1, 1, 8>(a, st);
     if (n * m <= 512) return few<T, 1, 1, 8>(a, st);
-    if (n * m <= 2048) return n >= 512 && m > 2 ? few<T, 2, 4, 8>(a, st) : few<T, 2, 2, 8>(a, st);
+    if ((n + 1) / 2 * ((m + 1) / 2) <= 512) return few<T, 2, 2, 8>(a, st);
     const struct { int bm, bn, step; } tiles[] = {{64, 64, 11}, {64, 128, 22}, {128, 128, 30}, {128, 256, 55}, {256, 256, 87}};
     int best = 0;
     long long least = 0, groups = 0;

@@ -1,0 +1,39 @@
+"""Products in 8-bit integers on both sides of the borders between their kernels, against 64 bits."""
+import pytest
+import torch
+
+import sequence_reference as ref
+import test_gpu_q8 as q8
+
+pytestmark = pytest.mark.gpu
+
+c2d = pytest.importorskip("conv2d_bias_activation_amd")
+
+
+def _check(kind, rows, k, n, act="none", before=False, shift=0):
+    dtype = q8.TYPES[kind]
+    x = q8._normal(rows + n, rows, k, dtype=dtype)
+    wcodes, wscales = q8._weights(n, n, k)
+    kw = {"bias": q8._normal(1, n, scale=0.1), "residual": q8._normal(2, rows, n, dtype=dtype),
+          "alpha": torch.rand(n, generator=torch.Generator().manual_seed(3)) if act == "prelu" else None}
+    want, bound = q8.product(*q8.quantized(x), wcodes, wscales, dtype, act=act, before=before, **kw)
+    dev = {name: q8._on(t) for name, t in kw.items()}
+    dev["residual"] = q8._wide(kw["residual"], 3, shift)
+    out = torch.full((rows + 1, n + 5), 7.0, dtype=dtype, device="cuda")
+    y = out[:rows, shift:shift + n]
+    c2d.matmul_q8(q8._wide(x, 2, shift), c2d.q8_pack(q8._on(wcodes), q8._on(wscales)), act=act, res_before_act=before, out=y,
+                  **dev)
+    ref.close(y, want, bound, f"{kind} {rows} x {k} -> {n}")
+    assert (out[rows] == 7).all() and (out[:, :shift] == 7).all() and (out[:, shift + n:] == 7).all()
+
+
+# rows and outputs in 16s: 2 x 256, 2 x 512 and 4 x 256 take the few-rows kernel, the sizes next to them tiles through LDS;
+# from 33 to 64 rows, outputs of some 8000 to 11000 are read twice by the one and once by the other
+@pytest.mark.parametrize("kind", list(q8.TYPES))
+@pytest.mark.parametrize("rows,k,n,more", [
+    (37, 100, 10007, {}), (33, 65, 8177, {"act": "prelu"}), (48, 129, 10912, {"act": "relu", "before": True}),
+    (33, 64, 8192, {"shift": 1}), (64, 320, 8192, {"act": "silu"}), (49, 200, 8193, {"act": "prelu", "before": True, "shift": 1}),
+    (17, 70, 16384, {}), (32, 70, 16385, {"shift": 2}), (65, 130, 5453, {"act": "relu"}), (65, 130, 5441, {}),
+    (128, 190, 4096, {"act": "prelu"}), (129, 190, 4096, {"shift": 1}), (127, 90, 4100, {"act": "silu", "before": True})])
+def test_next_to_the_few_rows_border(kind, rows, k, n, more):
+    _check(kind, rows, k, n, **more)
