@@ -725,10 +725,10 @@ template <typename T> hipError_t launch_direct(const Q8Args &p, const matmul_q8_
 //      33 x  4010 -> 13000                     20.0   15.1            814
 //     256 x  2048 ->  4096       12.9   10.4    9.0    8.2   14.4    1024
 // Among the tiles the one is taken whose workgroups, spread over the 256 CUs, take the least time
-// by what a step of 64 inputs of one takes where the card is full: 64x64 0.11 us, 64x128 0.22,
-// 128x128 0.30, 128x256 0.55, 256x256 0.87. Larger tiles read each operand less often; smaller ones
+// by what a step of 64 inputs of one takes where the card is full: 64x64 0.11 us, 128x128 0.30,
+// 128x256 0.55, 256x256 0.87. Larger tiles read each operand less often; smaller ones
 // make more workgroups. (2048 x 4096 -> 4096: 128x128 41.3 us, 128x256 40.5, 256x256 53.7; 1024 x 2048
-// -> 4096: 64x64 21, 64x128 17.1, 128x128 17.5; 4096 x 4096 -> 16384: 128x128 362, 128x256 334, 256x256
+// -> 4096: 64x64 21, 128x128 17.5; 4096 x 4096 -> 16384: 128x128 362, 128x256 334, 256x256
 // 262.) 64x64 tiles with three stages of the ring, for three workgroups a CU, where there are more of them than CUs,
 // else with four (256 x 2048 -> 4096 8.2 and 7.8 us, 333 x 2048 -> 4096 9.9 and 10.4, 1000 x 2048 -> 2048 10.5 and 11.0).
 template <typename T> hipError_t launch_product(const Q8Args &a, hipStream_t st) {
@@ -736,19 +736,18 @@ template <typename T> hipError_t launch_product(const Q8Args &a, hipStream_t st)
     if (m == 1) return n >= 1024 ? few<T, 2, 1, 8>(a, st) : few<T, 1, 1, 8>(a, st);
     if (n * m <= 512) return few<T, 1, 1, 8>(a, st);
     if ((n + 1) / 2 * ((m + 1) / 2) <= 512) return few<T, 2, 2, 8>(a, st);
-    const struct { int bm, bn, step; } tiles[] = {{64, 64, 11}, {64, 128, 22}, {128, 128, 30}, {128, 256, 55}, {256, 256, 87}};
+    const struct { int bm, bn, step; } tiles[] = {{64, 64, 11}, {128, 128, 30}, {128, 256, 55}, {256, 256, 87}};
     int best = 0;
     long long least = 0, groups = 0;
-    for (int i = 0; i < 5; i++) {
+    for (int i = 0; i < 4; i++) {
         const long long blocks = ((a.rows + tiles[i].bm - 1ll) / tiles[i].bm) * ((a.outs + tiles[i].bn - 1ll) / tiles[i].bn);
         const long long time = (blocks + 255) / 256 * tiles[i].step;
         if (i == 0 || time < least) best = i, least = time, groups = blocks;
     }
     switch (best) {
     case 0: return groups > 256 ? tiled<T, 64, 64, 2, 2, 3, 2>(a, st) : tiled<T, 64, 64, 2, 2, 4, 2>(a, st);
-    case 1: return tiled<T, 64, 128, 2, 2, 4, 1>(a, st);
-    case 2: return tiled<T, 128, 128, 2, 2, 4, 1>(a, st);
-    case 3: return tiled<T, 128, 256, 2, 4, 6, 1>(a, st);
+    case 1: return tiled<T, 128, 128, 2, 2, 4, 1>(a, st);
+    case 2: return tiled<T, 128, 256, 2, 4, 6, 1>(a, st);
     default: return tiled<T, 256, 256, 2, 4, 4, 1>(a, st);
     }
 }

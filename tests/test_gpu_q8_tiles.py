@@ -37,3 +37,12 @@ def _check(kind, rows, k, n, act="none", before=False, shift=0):
     (128, 190, 4096, {"act": "prelu"}), (129, 190, 4096, {"shift": 1}), (127, 90, 4100, {"act": "silu", "before": True})])
 def test_next_to_the_few_rows_border(kind, rows, k, n, more):
     _check(kind, rows, k, n, **more)
+
+
+# one size for each kernel and tile that a product may take, rows, inputs and outputs ending inside it: few rows of 1 x 1, 2 x 1
+# and 2 x 2 output tiles, then 64 x 64 (up to 256 workgroups and more), 128 x 128, 128 x 256 and 256 x 256
+@pytest.mark.parametrize("kind", list(q8.TYPES))
+@pytest.mark.parametrize("rows,k,n", [(9, 70, 2001), (9, 70, 16390), (90, 200, 2030), (199, 65, 4090), (340, 65, 4090),
+                                      (1020, 130, 4090), (4090, 70, 2039), (2040, 130, 8190)])
+def test_every_tile(kind, rows, k, n):
+    _check(kind, rows, k, n, act="prelu", shift=1)
