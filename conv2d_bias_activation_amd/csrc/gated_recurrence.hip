@@ -890,6 +890,10 @@ struct BackLayout {
 BackLayout back_layout(const gated_recurrence_backward_args &a) {
     BackLayout l{};
     l.k = plan(a, kGradient, true, &l.vec);
+    if (a.nseq == 0) {  // no chunks: only a bias gradient of zeros is written
+        l.k.items = 0;
+        return l;
+    }
     l.rec = record_bytes(l.k, 3, a.channels);
     const long long tiles = a.offsets ? a.tokens / kTile + a.nseq : (a.tokens + kTile - 1) / kTile * a.nseq;
     l.tile = ((size_t)tiles * 2 * a.channels * 4 + 255) / 256 * 256;
