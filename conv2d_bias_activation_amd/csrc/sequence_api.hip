@@ -236,14 +236,28 @@ int check_recurrence(const gated_recurrence_args *args, const char *op, bool ste
     return rc;
 }
 
-// Whether the rows of two outputs share a value: neither apart as wholes nor column slices of
-// the same wider rows.
+// Whether the rows of two outputs of the same width, neither of which overlap among themselves, share a value.
+// Rows with other strides are taken to.
 bool rows_share(const Shape &s, const Rows &a, long long abytes, const Rows &b, long long bbytes) {
     if (!overlap(a.p, abytes, b.p, bbytes)) return false;
-    if (a.token != b.token || (!s.step && !s.packed && a.batch != b.batch)) return true;
-    const Rows &lo = (uintptr_t)a.p <= (uintptr_t)b.p ? a : b, &hi = &lo == &a ? b : a;
-    const long long apart = (long long)((uintptr_t)hi.p - (uintptr_t)lo.p) / dtype_bytes(s.dtype);
-    return apart < lo.width || !rows_disjoint(s, Rows{lo.name, lo.p, lo.batch, lo.token, apart + hi.width});
+    const long long nb = s.packed ? 1 : s.nseq, nt = s.tokens, w = a.width;
+    if ((nt > 1 && a.token != b.token) || (nb > 1 && a.batch != b.batch)) return true;
+    const uintptr_t pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
+    const long long apart = (long long)(pa < pb ? pb - pa : pa - pb) / dtype_bytes(s.dtype);
+    // One axis steps over all rows of the other. Of its steps only the two next to the distance lead near enough to
+    // it, then of the other axis' only the two next to what is left.
+    const bool by_batch = nb > 1 && (nt <= 1 || a.batch >= (__int128)(nt - 1) * a.token + w);
+    const long long no = by_batch ? nb : nt, outer = by_batch ? a.batch : a.token;
+    const long long ni = by_batch ? nt : nb, inner = by_batch ? a.token : a.batch;
+    const long long q0 = no > 1 ? apart / outer : 0;
+    for (long long q = q0; q <= q0 + 1 && q < no; q++) {
+        const long long d = apart - q * outer, left = d < 0 ? -d : d, r0 = ni > 1 ? left / inner : 0;
+        for (long long r = r0; r <= r0 + 1 && r < ni; r++) {
+            const long long e = left - r * inner;
+            if (-w < e && e < w) return true;
+        }
+    }
+    return false;
 }
 
 int check_recurrence_backward(const gated_recurrence_backward_args *args, const char *op) {

@@ -351,9 +351,9 @@ def gated_recurrence_backward(grad, x, forget, *, gate=None, forget_bias=None, c
     it (None: the sequences started from zeros, as with ``fresh``) and is only read. ``grad_state``
     float32 [rows, channels] is updated in place, from the gradient of the state that a sequence
     left to that of the state it started from (None: the states left are of no further use).
-    ``out``: tensors (grad_x, grad_forget, grad_gate or None) to write, which may be column slices
-    of one tensor; grad_forget_bias is float32 and always new. ``workspace`` as for selective_scan,
-    but the call needs one, so not False."""
+    ``out``: tensors (grad_x, grad_forget, grad_gate or None) to write, which may be slices of one
+    tensor with the same strides; grad_forget_bias is float32 and always new. ``workspace`` as for
+    selective_scan, but the call needs one, so not False."""
     dt = _storage(x)
     dev, dtype, shape = x.device, x.dtype, x.shape
     nseq, tokens, *x_strides = _geometry(x, seq_offsets, False)

@@ -159,8 +159,8 @@ int gated_recurrence_step(const gated_recurrence_args *args, void *stream);
  * the state that it left (NULL: zero) and afterwards that with respect to the state, or the
  * zeros, that it started from.
  * Everything is fp32 but the values read and, rounded once each, grad_x, grad_forget and
- * grad_gate. The sum over tokens has a fixed order. The outputs may be column slices of one
- * tensor with the same strides (rows that interleave without sharing a value); they may overlap
+ * grad_gate. The sum over tokens has a fixed order. The outputs may be slices of one tensor with
+ * the same strides, their rows between each other's, as long as they share no value; they may overlap
  * no input. Needs gated_recurrence_backward_workspace_size() bytes of workspace, and returns
  * CONV2D_EUNSUPPORTED where the thread's is smaller. */
 typedef struct gated_recurrence_backward_args {
