@@ -17,6 +17,7 @@ import sys
 import time
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import conv2d_bias_activation_amd as c2d  # noqa: E402
@@ -29,6 +30,7 @@ class _Recurrence(torch.autograd.Function):
         return c2d.gated_recurrence(x, forget, gate=gate, forget_bias=forget_bias)
 
     @staticmethod
+    @once_differentiable  # the library has no gradient of the gradient
     def backward(ctx, grad):
         x, forget, gate, forget_bias = ctx.saved_tensors
         # one tensor for the three, as the projection that made them takes its gradient
