@@ -243,7 +243,7 @@ int q8_unpack(const void *packed, void *codes, float *scales, int rows, int in_f
  * The sums are exact; what follows is fp32, rounded once to y. The rows are x, quantized by the
  * call as quantize_rows does (it needs matmul_q8_workspace_size() bytes of workspace, 0 for a few
  * rows, or returns CONV2D_EUNSUPPORTED), or x_packed, for several products of the same rows. A
- * row or an output whose scale is NaN gives NaN. */
+ * row or an output whose scale is NaN is NaN before the activation, which keeps it but for ReLU's 0. */
 typedef struct matmul_q8_args {
     const void *x;         /* [rows, in_features], rows x_row elements apart, or NULL */
     const void *x_packed;  /* where x is NULL: packed rows, with the same sizes */

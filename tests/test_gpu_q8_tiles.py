@@ -46,3 +46,20 @@ def test_next_to_the_few_rows_border(kind, rows, k, n, more):
                                       (1020, 130, 4090), (4090, 70, 2039), (2040, 130, 8190)])
 def test_every_tile(kind, rows, k, n):
     _check(kind, rows, k, n, act="prelu", shift=1)
+
+
+@pytest.mark.parametrize("rows", [3, 40, 340])
+def test_rows_without_a_scale_through_the_epilogue(rows):
+    """A row with a NaN is NaN before the activation; ReLU makes 0 of a NaN here as in the convolutions, the others keep it."""
+    x = q8._normal(1, rows, 70)
+    x[1, 5] = float("nan")
+    w = c2d.q8_pack(*map(q8._on, q8._weights(1, 4090, 70)))
+    r = q8._on(q8._normal(2, rows, 4090))
+    alpha = torch.full((4090,), 0.5, device="cuda")
+    for act, kw in (("none", {}), ("silu", {}), ("prelu", {"alpha": alpha})):
+        y = c2d.matmul_q8(q8._on(x), w, residual=r, act=act, **kw)
+        assert torch.isnan(y[1]).all() and not torch.isnan(y[[0, 2]]).any(), act
+    y = c2d.matmul_q8(q8._on(x), w, residual=r, act="relu")
+    assert torch.equal(y[1], r[1])
+    y = c2d.matmul_q8(q8._on(x), w, residual=r, act="relu", res_before_act=True)
+    assert (y[1] == 0).all()
