@@ -215,7 +215,7 @@ __device__ __forceinline__ Floats<VEC> fold(const float *rec, long long stride, 
 
 // The first pass over split sequences, which leaves the chunks' records. A wave takes an eighth of
 // the chunk and needs the others at the end only: no barriers, and tokens that nobody writes for.
-// Bound by HBM: 65536 x 1024 bf16 in 50 us, 5.3 TB/s, the vector ALU 46 % busy.
+// Bound by HBM: 65536 x 1024 bf16 in 50 to 52 us, 5.2 to 5.4 TB/s, the vector ALU 52 % busy.
 template <typename T, int VEC, bool COUPLED>
 __global__ __launch_bounds__(64 * kNW) void rec_first_kernel(const gated_recurrence_args a, const RecCut k) {
     __shared__ float2 s_run[kNW][VEC][64];
@@ -288,10 +288,10 @@ __global__ __launch_bounds__(64 * kNW) void rec_first_kernel(const gated_recurre
 
 // The pass that writes y and the states. The eight waves of a tile take eight tokens each, so that a
 // workgroup's loads and stores stand side by side and the next tile's are on their way over the one
-// barrier of a tile (its LDS buffer alternates). Bound by HBM: 65536 x 1024 bf16 in 102 us behind the first
-// pass, 5.2 TB/s; the vector ALU is 52 % busy, whence one exponential and one reciprocal a gate. Two
-// workgroups a CU, for which registers are held to 128. Whole sequences need no first pass: 32768
-// tokens x 4096 in ragged sequences 226 us, 4.7 TB/s, with fewer workgroups towards the end.
+// barrier of a tile (its LDS buffer alternates). Bound by HBM: 65536 x 1024 bf16 in 103 to 111 us behind the
+// first pass, 4.8 to 5.2 TB/s; the vector ALU is 54 % busy, whence one exponential and one reciprocal a gate.
+// Two workgroups a CU, for which registers are held to 128. Whole sequences need no first pass: 32768
+// tokens x 4096 in ragged sequences 227 to 230 us, 4.7 TB/s, with fewer workgroups towards the end.
 template <typename T, int VEC, bool COUPLED, bool GATED>
 __global__ __launch_bounds__(64 * kNW, 4) void rec_prompt_kernel(const gated_recurrence_args a, const RecCut k) {
     __shared__ float2 s_run[2][kNW][VEC][64];
@@ -393,8 +393,8 @@ __global__ __launch_bounds__(64 * kNW, 4) void rec_prompt_kernel(const gated_rec
 
 // The first pass of the gradient walks forwards: it leaves, for each tile, the state before it as
 // an affine map of the state before the chunk, and, for split sequences, the chunks' records. A map
-// of 8 bytes for 64 tokens spares the second pass a walk of its own. HBM: 8 x 4096 x 2048 bf16 in 122 us,
-// 4.4 TB/s, the vector ALU 46 % busy. (A wave with an eighth of the chunk to itself, without the tile's
+// of 8 bytes for 64 tokens spares the second pass a walk of its own. HBM: 8 x 4096 x 2048 bf16 in 125 us,
+// 4.3 TB/s, the vector ALU 47 % busy. (A wave with an eighth of the chunk to itself, without the tile's
 // barrier, as in rec_first_kernel: 3 to 5 % slower for the whole call, whose second pass starts where
 // the workgroups' last tiles may still be cached.)
 template <typename T, int VEC, bool GATED, bool SPLIT>
@@ -507,8 +507,11 @@ __global__ __launch_bounds__(64 * kNW) void rec_back_first_kernel(const gated_re
 
 // The second pass walks backwards over the tiles and writes the gradients: the states before each
 // token again from the tile's, and the carry against them, both composed over the waves from the
-// same LDS records. Four inputs on their way and four values a token kept take 256 registers, so one
-// workgroup a CU. HBM: 8 x 4096 x 2048 bf16 in 184 us, 5.1 TB/s, the vector ALU 53 % busy. WHOLE: the channels
+// same LDS records. Four inputs on their way and four values a token kept take 250 registers in f16, so one
+// workgroup a CU, and in gated bf16 256 and 12 to 24 bytes a lane spilled. Forms without the spill are no faster: with the
+// records of one direction read before the other's (231 registers) 8 x 4096 x 2048 takes 311 us, not 309, 64 ragged
+// sequences of 16000 x 1500 148, not 141; with x unpacked again for each use (251) 310 and 141.
+// HBM: 8 x 4096 x 2048 bf16 in 178 to 182 us, 5.2 TB/s, the vector ALU 56 % busy. WHOLE: the channels
 // fill their blocks, which all waves would ask otherwise (a gradient of 8 x 4096 x 2048 in 313 us, not 323); else the
 // waves whose lanes all own theirs still store without a look at each (8 x 4096 x 2112 352 us, not 392).
 template <typename T, int VEC, bool WHOLE, bool GATED>
@@ -678,8 +681,9 @@ __global__ __launch_bounds__(64 * kNW) void rec_back_kernel(const gated_recurren
     if (wave == 0 && grad_state && p.chunk == 0) put<float, VEC>(grad_state, carry, own);
 }
 
-// Sums of `items` rows of partial sums, in a fixed order. 2 to 5 us, of which most is the launch and the
-// first access; atomics in the second pass would save it and lose the order.
+// Sums of `items` rows of partial sums, in a fixed order. 1.5 to 4.6 us, of which most is the launch and the
+// first access. Sums by atomics in the second pass would have no order; a ticket, with the last workgroup of a block of
+// channels adding the rows, would have this one and no launch (not built).
 __global__ __launch_bounds__(1024) void rec_bias_kernel(const float *part, float *out, int items, int channels) {
     __shared__ float s[16][64];
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
@@ -743,18 +747,18 @@ struct Costs {
 };
 // Measured, bf16, us whole / split:
 //   sequences x tokens x channels   prompt             gradient
-//   1 x 256 x 1024                  11.8 /   9.7       40 /  19
-//   1 x 4096 x 1024                  147 /  17         368 /  31
-//   32 x 512 x 2048                   45 /  47         138 / 137
-//   12 x 1000 x 1280                  44 /  38         115 /  83
-//   8 x 4096 x 2048                  170 / 133         513 / 305
-//   8 x 4096 x 2176                  178 / 157         460 / 343
-//   16 x 2048 x 2176                 159 / 152         410 / 350
-//   16 x 2048 x 4096, ragged         238 / 341         573 / 694
-//   64 x 250 x 1500, ragged           65 /  73         165 / 202
-//   40 x 1000 x 2112, ragged         194 / 211         474 / 554
-//   32 x 1000 x 1000, ragged         121 /  93         324 / 243
-//   1 x 65536 x 1024                2520 / 148        7030 / 307
+//   1 x 256 x 1024                   9.8 /   8.4       25 /  14
+//   1 x 4096 x 1024                  148 /  16         376 /  30
+//   32 x 512 x 2048                   46 /  68         128 / 170
+//   12 x 1000 x 1280                  43 /  39         105 /  74
+//   8 x 4096 x 2048                  174 / 138         464 / 312
+//   8 x 4096 x 2176                  177 / 163         452 / 342
+//   16 x 2048 x 2176                 156 / 156         406 / 353
+//   16 x 2048 x 4096, ragged         253 / 330         620 / 666
+//   64 x 250 x 1500, ragged           52 /  75         141 / 198
+//   40 x 1000 x 2112, ragged         159 / 205         387 / 530
+//   32 x 1000 x 1000, ragged         124 /  86         322 / 236
+//   1 x 65536 x 1024                2590 / 157        6510 / 331
 constexpr Costs kPrompt{3.0, 9.0, 2.2, 4.0, 4.7, true}, kGradient{8.0, 17.0, 5.8, 9.0, 10.3, false};
 
 constexpr int kWorkgroups = 256;        // that the card runs at full speed side by side: one for each CU

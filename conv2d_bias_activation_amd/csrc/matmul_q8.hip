@@ -137,8 +137,9 @@ template <typename T> __device__ __forceinline__ u32x4 codes16(const Pack<T, 16>
 // WPR waves a row, so that few rows still make many waves, and ROWS neighbouring rows a workgroup,
 // whose 16-byte records make whole runs of 64 or 128 bytes. NR groups of 16 values of a lane stay
 // in registers between the maximum and the codes; a longer row is read again. The values behind
-// the last whole group go to a lane each. 4096 x 4096 bf16 in 13.4 to 16 us (50 MB, 3.1 to 3.7 TB/s: HBM and the
-// vector ALU, some 14 instructions a value); 37 x 4010 in 4 us, a launch and two latencies.
+// the last whole group go to a lane each. 4096 x 4096 bf16 in 13.2 to 15.5 us (50 MB, 3.2 to 3.8 TB/s, the vector ALU 28 %
+// busy with some 14 instructions a value: neither is full, and what bounds it is not established); 37 x 4010 in 4 us, a
+// launch and two latencies.
 template <typename T, int WPR, int ROWS, int NR>
 __global__ __launch_bounds__(64 * WPR * ROWS) void quantize_kernel(const T *x, long long x_row, void *packed, int rows, int n) {
     __shared__ uint32_t s_most[WPR * ROWS];

@@ -13,6 +13,10 @@ not overlap one.
 A call on ``stream`` enqueues its work there (default: the device's current stream) and
 allocates what it returns there too; inputs made on another stream have to be waited for by
 the caller, as with any kernel.
+
+No call is recorded for torch's differentiation: what it returns requires no gradient, whatever its
+inputs do. Training through the gated recurrence calls gated_recurrence_backward, from a
+torch.autograd.Function as in examples/gated_recurrence_block.py.
 """
 from __future__ import annotations
 
@@ -331,7 +335,8 @@ def gated_recurrence(x, forget, *, gate=None, forget_bias=None, coupled=True, st
     (int32 [sequences + 1] on the GPU), of one dtype (float32, bfloat16 or float16), any strides
     but the last. forget_bias: float32 [channels]. ``state`` float32 [rows, channels] is read and
     updated in place; ``slots``, ``fresh``, ``longest`` and ``workspace`` as for selective_scan.
-    Returns y, shaped as x."""
+    Returns y, shaped as x, which has no history for torch's differentiation: the gradient is
+    gated_recurrence_backward. Rows that no packed sequence covers are not written."""
     return _recurrence("gated_recurrence", x, forget, gate, forget_bias, coupled, state, slots, fresh, seq_offsets, longest,
                        out, stream, workspace, False)
 
@@ -352,8 +357,9 @@ def gated_recurrence_backward(grad, x, forget, *, gate=None, forget_bias=None, c
     float32 [rows, channels] is updated in place, from the gradient of the state that a sequence
     left to that of the state it started from (None: the states left are of no further use).
     ``out``: tensors (grad_x, grad_forget, grad_gate or None) to write, which may be slices of one
-    tensor with the same strides; grad_forget_bias is float32 and always new. ``workspace`` as for
-    selective_scan, but the call needs one, so not False."""
+    tensor with the same strides; grad_forget_bias is float32 and always new. Rows that no packed
+    sequence covers are not written. ``workspace`` as for selective_scan, but the call needs one,
+    so not False."""
     dt = _storage(x)
     dev, dtype, shape = x.device, x.dtype, x.shape
     nseq, tokens, *x_strides = _geometry(x, seq_offsets, False)
